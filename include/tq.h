@@ -496,6 +496,127 @@ int tq_fq_dequantize(const tq_fq_codec *codec, const tq_cache *cache, int which,
                      int64_t rows, float *out, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Ragged batches over a paged cache.
+ *
+ * A server keeps the tokens of many sequences in pages of one pool and, in
+ * each step, adds some new tokens to each sequence: whole prompts, chunks of
+ * prompts, drafted tokens, or one token a sequence.  A paged cache is a
+ * tq_cache whose batch index is a page: B pages of rows_cap tokens each
+ * (rows_cap a power of two, 32 to 2^20), planes as above.  Token t of a
+ * sequence is row t % rows_cap of page page_table[s][t / rows_cap].
+ *
+ * tq_paged_batch describes one step.  The new tokens of the num_seqs
+ * sequences are rows of the packed tensors, sequence s at rows q_start[s] ..
+ * q_start[s + 1] - 1; it holds seq_lens[s] cached tokens once they are
+ * appended, so its new token i sits at position
+ * seq_lens[s] - (q_start[s + 1] - q_start[s]) + i.
+ *   page_table  device int32 [num_seqs] rows of max_pages entries,
+ *               table_stride elements apart.  Sequences may share pages that
+ *               none of them writes in the call.
+ *   q_start     device int32 [num_seqs + 1], non-decreasing.
+ *   seq_lens    device int32 [num_seqs].
+ *   max_new     no sequence has more new tokens; rows beyond it are left out.
+ *   max_seq_len no sequence is longer (entries are clamped); at most
+ *               max_pages * rows_cap.
+ * The arrays are read by the kernels only, so a captured call follows their
+ * contents at replay; no contents lead to an access outside the buffers.  A
+ * page number outside the pool stands for a page that is not there: its
+ * tokens are not written, not seen by any query, and read back as zeros.  Where
+ * seq_lens[s] is smaller than the new tokens, the first ones have no position:
+ * not written, zeros as the answer.  Packed rows that belong to no sequence,
+ * those behind the last one among them, are left as they were.  num_tokens is the row
+ * count of the packed tensors (at most 2^24; at most 65535 sequences).
+ * Supported: d = 64 and 128, every key and value width, with and without the
+ * sketch, Walsh-Hadamard and dense rotations.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const int32_t *page_table;
+  const int32_t *q_start;
+  const int32_t *seq_lens;
+  int64_t table_stride;
+  int num_seqs;
+  int max_pages;
+  int max_new;
+  int max_seq_len;
+} tq_paged_batch;
+
+/* Append the new tokens' keys and values to their pages.
+ * k, v      device, [num_tokens][Hkv][d] with element strides stride_t and
+ *           stride_h (both tensors) and d contiguous; TQ_F32 or TQ_BF16.
+ * rope_cos, rope_sin  device fp32 [rope_len][d/2], nullable together: keys are
+ *           rotated at their positions first; rope_len >= max_seq_len.
+ * Codes and signs are those of exact arithmetic on the inputs (fp32 first,
+ * 64-bit arithmetic for a row with a value near a border), so a token's bytes
+ * do not depend on the batch or chunk it arrives in; nu and rho are rounded
+ * to fp16 from fp32 or 64-bit values and may differ in the last bit.
+ * Other tokens of a partly covered 32-token value group are preserved; calls
+ * that touch the same page must be stream-ordered, and a token written by two
+ * sequences of one call has unspecified codes.
+ * status    device uint32, nullable: incremented once per row (key or value
+ *           of a token and head) that had a non-finite element or whose fp16
+ *           norm overflowed (encoded as the zero row), or that had no page. */
+int tq_paged_quantize_kv(const tq_codec *codec, const void *k, const void *v, int dtype,
+                         int num_tokens, int64_t stride_t, int64_t stride_h,
+                         const float *rope_cos, const float *rope_sin, int rope_len,
+                         const tq_cache *cache, const tq_paged_batch *batch, uint32_t *status,
+                         void *stream);
+
+/* The batch's rows read back as vectors (tq_dequantize through the page
+ * table): with q_start the running sum of seq_lens, whole sequences.
+ * k_out, v_out  device [num_tokens][Hkv][d], out_dtype, 16-byte aligned; one
+ *           of them may be NULL. */
+int tq_paged_dequantize(const tq_codec *codec, const tq_cache *cache, const tq_paged_batch *batch,
+                        int num_tokens, void *k_out, void *v_out, int out_dtype, void *stream);
+
+/* Attention of the new tokens over the pages: the query of a new token at
+ * position t sees cached tokens 0 .. t of its sequence (the new ones must
+ * have been appended), with the estimator of tq_attention_decode.
+ * q         device [num_tokens][Hq][d] with element strides stride_t,
+ *           stride_h; TQ_F32 or TQ_BF16.  rope_cos, rope_sin as above.
+ * out       device [num_tokens][Hq][d], out_dtype, 16-byte aligned.  A query
+ *           that sees no token gets zeros.
+ * workspace device, >= tq_paged_attention_workspace(...) bytes for the same
+ *           batch limits, 16-byte aligned; needs no initialisation.  Calls
+ *           that may run at the same time need workspaces of their own.
+ * Products run on the tensor cores from fp16 and bf16 operands with fp32
+ * sums: about 2e-3 of the output's norm for logits of a few tens. */
+int tq_paged_attention_workspace(const tq_codec *codec, const tq_paged_batch *batch,
+                                 int num_tokens, int Hq, int Hkv, size_t *bytes);
+int tq_paged_attention(const tq_codec *codec, const void *q, int dtype, int num_tokens, int Hq,
+                       int64_t stride_t, int64_t stride_h, const tq_cache *cache,
+                       const tq_paged_batch *batch, float scale, const float *rope_cos,
+                       const float *rope_sin, int rope_len, void *workspace, size_t ws_bytes,
+                       void *out, int out_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * RMS norm of every query and key head, then the position rotation, in one
+ * pass (models that norm their heads; the rotation follows the norm, so the
+ * calls above then take the results without a rope table):
+ *   y = x w / sqrt(mean(x^2) + eps),
+ *   out_i = y_i cos - y_{i+d/2} sin, out_{i+d/2} = y_{i+d/2} cos + y_i sin.
+ * q, k      nullable (not both).  x, y: device [num_tokens][heads][d] with
+ *           element strides, d contiguous, dtype; y may be x itself (same
+ *           strides), otherwise they do not overlap.  weight: device [d] of
+ *           weight_dtype, nullable (ones).
+ * positions device int32 [num_tokens], clamped to 0 .. rope_len - 1; may be
+ *           NULL without a table.  rope_cos, rope_sin  device fp32
+ *           [rope_len][d/2], nullable together (norm only).
+ * Sums and products in fp32, one rounding to dtype.  d = 64 or 128.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const void *x;
+  void *y;
+  const void *weight;
+  int64_t x_stride_t, x_stride_h;
+  int64_t y_stride_t, y_stride_h;
+  int heads;
+} tq_heads;
+
+int tq_qk_norm_rope(const tq_heads *q, const tq_heads *k, int dtype, int weight_dtype, int d,
+                    int num_tokens, float eps, const int32_t *positions, const float *rope_cos,
+                    const float *rope_sin, int rope_len, void *stream);
+
+/* ------------------------------------------------------------------------
  * Profiling hooks (no counterpart on the pages; used by the benchmark).
  * tq_set_timing_events: when both are non-NULL, every later
  *   tq_attention_decode / tq_attention_logits on this thread records `start`

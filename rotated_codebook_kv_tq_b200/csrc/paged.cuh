@@ -1,0 +1,71 @@
+// Device view of a ragged batch over a paged cache (tq_paged_batch): which
+// cache row a token sits in, which new tokens a sequence has.  Every value
+// read from device memory (starts, lengths, page numbers) is clamped or
+// checked here, so no batch takes an access out of its buffers.
+#pragma once
+
+#include "tq_device.cuh"
+
+struct PagedView {
+  const int32_t *table;    // [num_seqs][table_stride] page numbers
+  const int32_t *q_start;  // [num_seqs + 1]
+  const int32_t *seq_lens; // [num_seqs]
+  int64_t table_stride;
+  int num_seqs;
+  int max_pages;
+  int max_new;
+  int max_len;
+  int N;                   // rows of the packed tensors
+  int num_pages;           // pages of the pool
+  int page_shift;          // page size = 2^page_shift
+};
+
+struct SeqSpan {
+  int row0;   // first packed row
+  int n;      // new tokens
+  int len;    // cached tokens, the new ones included
+};
+
+__device__ __forceinline__ SeqSpan paged_span(const PagedView &p, int s) {
+  SeqSpan r;
+  const int a = min(max(p.q_start[s], 0), p.N);
+  const int b = min(max(p.q_start[s + 1], a), p.N);
+  r.row0 = a;
+  r.n = min(b - a, p.max_new);
+  r.len = min(max(p.seq_lens[s], 0), p.max_len);
+  return r;
+}
+
+// Pool page of the sequence's token `pos` (0 <= pos < max_len), or -1 where
+// the table names none.
+__device__ __forceinline__ int paged_page(const PagedView &p, int s, int pos) {
+  const int pg = p.table[s * p.table_stride + (pos >> p.page_shift)];
+  return static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages) ? pg : -1;
+}
+
+// Units of `per` packed rows (plus `slack` for the ends of a sequence) are
+// numbered so that sequence s starts at unit q_start[s] / per + slack * s:
+// the sequences' unit ranges do not overlap, and their number has a bound
+// known on the host (units_bound).  Unit u belongs to the last sequence that
+// starts at or before it; found by a 32-way search of the calling warp.
+__host__ __device__ inline int64_t paged_units_bound(int64_t N, int per, int slack, int num_seqs) {
+  return N / per + static_cast<int64_t>(slack) * num_seqs;
+}
+
+__device__ __forceinline__ int paged_unit_base(const PagedView &p, int s, int per, int slack) {
+  return min(max(p.q_start[s], 0), p.N) / per + slack * s;
+}
+
+__device__ __forceinline__ int paged_find_seq(const PagedView &p, int u, int per, int slack) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.num_seqs;   // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && paged_unit_base(p, at, per, slack) <= u;
+    const int k = 31 - __clz(__ballot_sync(TQ_FULL, below) | 1u);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}

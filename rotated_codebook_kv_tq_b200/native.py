@@ -29,7 +29,8 @@ EXPORTS = [
     "tq_quantize_kv_split", "tq_attention_split_workspace", "tq_attention_decode_split",
     "tq_dequantize_split", "tq_haar_rotation", "tq_fq_build_codebook", "tq_fq_codec_create", "tq_fq_codec_destroy",
     "tq_fq_codec_codebooks", "tq_fq_cache_bytes", "tq_fq_quantize_kv", "tq_fq_attention_workspace",
-    "tq_fq_attention_decode", "tq_fq_dequantize", "tq_set_timing_events", "tq_launch_count",
+    "tq_fq_attention_decode", "tq_fq_dequantize", "tq_paged_quantize_kv", "tq_paged_dequantize",
+    "tq_paged_attention_workspace", "tq_paged_attention", "tq_qk_norm_rope", "tq_set_timing_events", "tq_launch_count",
     "tq_last_error",
 ]
 
@@ -59,6 +60,20 @@ class FqCodecDesc(ctypes.Structure):
 
 class SplitDesc(ctypes.Structure):
     _fields_ = [("hi", ctypes.c_void_p), ("lo", ctypes.c_void_p), ("channels", ctypes.c_void_p)]
+
+
+class PagedBatchDesc(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("max_seq_len", ctypes.c_int)]
+
+
+class HeadsDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_stride_t", ctypes.c_int64), ("x_stride_h", ctypes.c_int64),
+                ("y_stride_t", ctypes.c_int64), ("y_stride_h", ctypes.c_int64),
+                ("heads", ctypes.c_int)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -123,6 +138,13 @@ def lib() -> ctypes.CDLL:
         L.tq_fq_attention_workspace.argtypes = [vp, i32, i32, i32, ctypes.POINTER(sz)]
         L.tq_fq_attention_decode.argtypes = L.tq_attention_decode.argtypes
         L.tq_fq_dequantize.argtypes = L.tq_dequantize.argtypes
+        bp, hp = ctypes.POINTER(PagedBatchDesc), ctypes.POINTER(HeadsDesc)
+        L.tq_paged_quantize_kv.argtypes = [vp, vp, vp, i32, i32, i64, i64, vp, vp, i32, cp, bp, vp, vp]
+        L.tq_paged_dequantize.argtypes = [vp, cp, bp, i32, vp, vp, i32, vp]
+        L.tq_paged_attention_workspace.argtypes = [vp, bp, i32, i32, i32, ctypes.POINTER(sz)]
+        L.tq_paged_attention.argtypes = [vp, vp, i32, i32, i32, i64, i64, cp, bp, f32, vp, vp, i32, vp,
+                                         sz, vp, i32, vp]
+        L.tq_qk_norm_rope.argtypes = [hp, hp, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp]
         L.tq_set_timing_events.argtypes = [vp, vp]
         L.tq_launch_count.argtypes = []
         L.tq_launch_count.restype = ctypes.c_uint64
@@ -608,6 +630,155 @@ def fq_dequantize(codec: FqCodec, cache: Cache, which: int, row0: int, rows: int
     desc = cache.desc()
     check(lib().tq_fq_dequantize(codec.handle, ctypes.byref(desc), which, row0, rows, _ptr(out),
                                  _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged cache
+
+@dataclass
+class PagedBatch:
+    """A ``tq_paged_batch``: the new tokens of several sequences over a paged
+    cache (an ``alloc_cache`` whose batch is the page pool and whose rows_cap is
+    the page size).  page_table int32 [S, max_pages], q_start int32 [S + 1],
+    seq_lens int32 [S] are device tensors, read when the kernels run; max_new
+    and max_seq_len are their host-side limits."""
+    page_table: "object"
+    q_start: "object"
+    seq_lens: "object"
+    max_new: int
+    max_seq_len: int
+
+    def desc(self) -> PagedBatchDesc:
+        t = self.page_table
+        key = (t.data_ptr(), self.q_start.data_ptr(), self.seq_lens.data_ptr(), t.stride(0),
+               self.seq_lens.shape[0], t.shape[1], self.max_new, self.max_seq_len)
+        cached = self.__dict__.get("_desc")
+        if cached is None or cached[0] != key:
+            self._check()
+            cached = (key, PagedBatchDesc(*key))
+            self.__dict__["_desc"] = cached
+        return cached[1]
+
+    def _check(self) -> None:
+        import torch
+        t, S = self.page_table, self.seq_lens.shape[0]
+        if any(x.dtype != torch.int32 for x in (t, self.q_start, self.seq_lens)):
+            raise TypeError("page_table, q_start and seq_lens must be int32")
+        if t.dim() != 2 or t.shape[0] != S or self.q_start.shape != (S + 1,) or self.seq_lens.dim() != 1:
+            raise ValueError("page_table [S, max_pages], q_start [S + 1] and seq_lens [S] go together")
+        if (t.shape[1] > 1 and t.stride(1) != 1) or not (self.q_start.is_contiguous() and
+                                                         self.seq_lens.is_contiguous()):
+            raise ValueError("page_table rows, q_start and seq_lens must be contiguous")
+
+
+def _packed(name: str, t, d: int):
+    """Strides (token, head) of a packed [N, H, d] tensor with d contiguous."""
+    if t.dim() != 3 or t.shape[2] != d or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, {d}] with the last dim contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def _rope_args(rope, d: int):
+    if rope is None:
+        return None, None, 0
+    c, s = rope
+    if c.shape != s.shape or c.dim() != 2 or c.shape[1] != d // 2 or not (c.is_contiguous() and s.is_contiguous()) \
+            or _dtype_code(c) != TQ_F32 or _dtype_code(s) != TQ_F32:
+        raise ValueError(f"rope must be two contiguous fp32 tables [positions, {d // 2}]")
+    return c.data_ptr(), s.data_ptr(), c.shape[0]
+
+
+def paged_quantize_kv(codec: Codec, k, v, cache: Cache, batch: PagedBatch, rope=None, status=None,
+                      stream=None) -> None:
+    """tq_paged_quantize_kv: the new tokens' k, v [N, Hkv, d] (same strides)
+    coded into their pages, keys rotated at their positions first."""
+    N, H, d = k.shape
+    st, sh = _packed("k", k, codec.d)
+    if v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or H != cache.Hkv:
+        raise ValueError("k and v need the same shape, strides and dtype, and the cache's KV heads")
+    rc, rs, rn = _rope_args(rope, codec.d)
+    check(lib().tq_paged_quantize_kv(codec.handle, k.data_ptr(), v.data_ptr(), _dtype_code(k), N, st, sh,
+                                     rc, rs, rn, ctypes.byref(cache.desc()), ctypes.byref(batch.desc()),
+                                     _ptr(status), _stream(stream)))
+
+
+def paged_dequantize(codec: Codec, cache: Cache, batch: PagedBatch, k_out, v_out, stream=None) -> None:
+    """tq_paged_dequantize: the batch's rows as vectors into k_out, v_out
+    [N, Hkv, d] (contiguous, fp32 or bf16; one may be None)."""
+    ref = k_out if k_out is not None else v_out
+    if ref is None:
+        raise ValueError("k_out or v_out is required")
+    for t in (k_out, v_out):
+        if t is not None and (tuple(t.shape) != (ref.shape[0], cache.Hkv, codec.d) or t.dtype != ref.dtype
+                              or not t.is_contiguous()):
+            raise ValueError(f"outputs must be contiguous [tokens, {cache.Hkv}, {codec.d}] of one dtype")
+    check(lib().tq_paged_dequantize(codec.handle, ctypes.byref(cache.desc()), ctypes.byref(batch.desc()),
+                                    ref.shape[0], _ptr(k_out), _ptr(v_out), _dtype_code(ref),
+                                    _stream(stream)))
+
+
+def paged_attention_workspace(codec: Codec, batch: PagedBatch, num_tokens: int, Hq: int, Hkv: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(lib().tq_paged_attention_workspace(codec.handle, ctypes.byref(batch.desc()), num_tokens, Hq, Hkv,
+                                             ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention(codec: Codec, q, cache: Cache, batch: PagedBatch, scale: float, out, workspace,
+                    rope=None, stream=None) -> None:
+    """tq_paged_attention: q [N, Hq, d] of the new tokens, each over the cached
+    tokens up to its own position -> out [N, Hq, d] (fp32 or bf16)."""
+    N, Hq, d = q.shape
+    st, sh = _packed("q", q, codec.d)
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous and shaped like q")
+    rc, rs, rn = _rope_args(rope, codec.d)
+    check(lib().tq_paged_attention(codec.handle, q.data_ptr(), _dtype_code(q), N, Hq, st, sh,
+                                   ctypes.byref(cache.desc()), ctypes.byref(batch.desc()), float(scale),
+                                   rc, rs, rn, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), out.data_ptr(),
+                                   _dtype_code(out), _stream(stream)))
+
+
+def _heads(name: str, x, y, w, d: int) -> Optional[HeadsDesc]:
+    if x is None:
+        return None
+    st, sh = _packed(name, x, d)
+    if y is None or y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError(f"{name}: the output must have the input's shape and dtype")
+    yt, yh = _packed(name, y, d)
+    if w is not None and (w.shape != (d,) or not w.is_contiguous()):
+        raise ValueError(f"{name}: the weight must be [{d}]")
+    return HeadsDesc(x.data_ptr(), y.data_ptr(), _ptr(w), st, sh, yt, yh, x.shape[1])
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, q_out, k_out, rope=None,
+                 stream=None) -> None:
+    """tq_qk_norm_rope: RMS norm of every head of q [N, Hq, d] and k [N, Hk, d]
+    (either may be None), then the rotation at positions int32 [N], into q_out
+    and k_out (which may be q and k)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k is required")
+    N, _, d = ref.shape
+    if q is not None and k is not None and (k.shape[0] != N or k.shape[2] != d or k.dtype != q.dtype):
+        raise ValueError("q and k need the same tokens, head dim and dtype")
+    w = q_weight if q_weight is not None else k_weight
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight need the same dtype")
+    rc, rs, rn = _rope_args(rope, d)
+    if positions is not None and (_is_int32(positions) is False or positions.shape != (N,)
+                                  or not positions.is_contiguous()):
+        raise ValueError("positions must be contiguous int32 [tokens]")
+    dq, dk = _heads("q", q, q_out, q_weight, d), _heads("k", k, k_out, k_weight, d)
+    check(lib().tq_qk_norm_rope(None if dq is None else ctypes.byref(dq),
+                                None if dk is None else ctypes.byref(dk), _dtype_code(ref),
+                                TQ_F32 if w is None else _dtype_code(w), d, N, float(eps), _ptr(positions),
+                                rc, rs, rn, _stream(stream)))
+
+
+def _is_int32(t) -> bool:
+    import torch
+    return t.dtype == torch.int32
 
 
 def set_timing_events(start=None, stop=None) -> None:
