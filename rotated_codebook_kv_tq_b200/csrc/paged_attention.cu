@@ -161,16 +161,23 @@ __global__ void __launch_bounds__(128) paged_attn_kernel(PagedAttnArgs a) {
   }
 }
 
+bool few_rows(int max_new, int Hq, int Hkv) { return static_cast<int64_t>(max_new) * (Hq / Hkv) <= 64; }
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(const tq_codec *c, int N, int num_seqs, int max_new, int max_len, int Hq,
                                   int Hkv) {
-  return 16;
+  if (N == 0 || num_seqs == 0 || max_new == 0) return 16;
+  return few_rows(max_new, Hq, Hkv)
+             ? paged_decode_workspace_bytes(c, N, num_seqs, max_new, max_len, Hq, Hkv)
+             : 16;
 }
 
 int launch_paged_attention(const tq_codec *c, const PagedView &p, const void *q, int dtype, int64_t st,
                            int64_t sh, int Hq, const tq_cache *cache, float scale, const float *rc,
                            const float *rs, void *ws, void *out, int out_dtype, cudaStream_t stream) {
+  if (few_rows(p.max_new, Hq, cache->Hkv))
+    return launch_paged_decode(c, p, q, dtype, st, sh, Hq, cache, scale, rc, rs, ws, out, out_dtype, stream);
   PagedAttnArgs a;
   a.p = p;
   a.q = q;

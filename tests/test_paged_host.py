@@ -126,6 +126,9 @@ def test_attention_refusals(L, codec):
     assert attention(L, c, wsb=n.value - 1) == native.TQ_ERR_WORKSPACE
     assert attention(L, c, ws=None) == native.TQ_ERR_WORKSPACE
     assert attention(L, c, ws=X + 8) == native.TQ_ERR_ALIGNMENT
+    # limits of empty and of very large steps
+    for kw in (dict(num_seqs=0), dict(max_new=0), dict(max_seq_len=0), dict(max_new=(1 << 31) - 1)):
+        assert L.tq_paged_attention_workspace(c, ctypes.byref(batch(**kw)), 8, 4, 2, ctypes.byref(n)) == native.TQ_OK
     for bad in (dict(N=-1), dict(Hq=3), dict(Hkv=0)):
         a = dict(N=8, Hq=4, Hkv=2)
         a.update(bad)
