@@ -49,3 +49,8 @@ size_t paged_decode_workspace_bytes(const tq_codec *c, int N, int num_seqs, int 
 int launch_paged_decode(const tq_codec *c, const PagedView &p, const void *q, int dtype, int64_t st, int64_t sh,
                         int Hq, const tq_cache *cache, float scale, const float *rc, const float *rs, void *ws,
                         void *out, int out_dtype, cudaStream_t stream);
+// Many query rows a KV head (paged_prefill.cu); at most 128 query heads a KV head.
+size_t paged_prefill_workspace_bytes(const tq_codec *c, int N, int num_seqs, int max_len, int Hq, int Hkv);
+int launch_paged_prefill(const tq_codec *c, const PagedView &p, const void *q, int dtype, int64_t st, int64_t sh,
+                         int Hq, const tq_cache *cache, float scale, const float *rc, const float *rs, void *ws,
+                         void *out, int out_dtype, cudaStream_t stream);

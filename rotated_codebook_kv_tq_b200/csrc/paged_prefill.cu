@@ -1,0 +1,750 @@
+// Attention of many new tokens over a paged compressed cache, in two steps.
+//
+// 1. The pages are expanded once into operand tiles of 128 tokens, in the
+//    rotated domain and in the layout that the tensor cores read:
+//      K^_j = 2^-E nu_j (c[idx_j] + coef rho_j S^T (2 sigma_j - 1))   fp16
+//      V^_j = 2^-F nu^v_j c_v[idx^v_j]                                 fp16, transposed
+//    with 2^E, 2^F just above the tile's largest norms, so entries are at most
+//    1 and a token far below the tile's largest loses only absolute precision
+//    (2^-25 of that largest).  The sketch's part of a logit,
+//    coef rho <S q', 2 sigma - 1>, becomes part of the key vector: a logit costs
+//    d products in place of 2 d, and the expansion is shared by all queries.
+// 2. Blocks of 2 x 128 query rows (a token's query heads of one KV head side by
+//    side) walk the tiles: S = q' K^T and O += P V by tcgen05.mma with fp32
+//    accumulators in tensor memory, P = 2^(S 2^E + F - M) written over S as the
+//    fp16 operand.  Two query tiles alternate, so the products of one run under
+//    the softmax of the other.
+// Statistics and sums are fp32.  Roundings to fp16: q' scale log2 e, K^, V^ and
+// P, 2^-11 of an element each.
+#include <math_constants.h>
+
+#include <cstdlib>
+
+#include "paged.h"
+#include "tq_sm100.cuh"
+
+namespace {
+
+constexpr int TK = 128;        // tokens of a tile
+constexpr int TQ = 128;        // query rows of a tile
+constexpr uint32_t HDR = 128;  // bytes before a tile's operands
+
+struct TileHeader {
+  float k_exp;       // 2^E
+  float v_exp;       // F
+  float v_inv;       // 2^-F
+  uint32_t all;      // every token of the tile is there
+  uint32_t there[4]; // bit per token
+};
+
+constexpr uint32_t tile_bytes(int d) { return HDR + 2u * TK * d * 2u; }
+
+struct PrefillArgs {
+  PagedView p;
+  const void *q;
+  int dtype;
+  int64_t st, sh;
+  int Hq, Hkv, G;
+  int head0, heads;          // KV heads of this pass
+  const uint8_t *kcode;
+  const uint16_t *kscale;
+  const uint32_t *vcode;
+  const uint16_t *vnorm;
+  float scale, qjl_coef;
+  const float *rc, *rs;
+  void *out;
+  int out_dtype;
+  const uint16_t *S;
+  uint8_t *tiles;            // [heads][num_seqs][max_tiles] tile images
+  int max_tiles;
+  int tok_tile;              // new tokens of a query tile: 128 / G
+  int units;                 // query tile pairs (bound)
+  int splits, chunk;         // token tiles of a block
+  float *po;                 // [N Hq][splits][D]
+  float2 *pml;
+  uint32_t wait_outer;
+  TqBooks books;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// ------------------------------------------------------------------ expansion
+
+// One block a token tile of a (sequence, KV head); EX tiles in a row share the
+// block's copy of S.
+constexpr int EX = 4;
+
+template <int D>
+__global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int NPL = D / 32, KS = D / 16, NN = D / 8;
+  extern __shared__ __align__(16) uint2 sfrag[];   // [KS][NN][32]
+  __shared__ float ckt[16], cvt[16], nuk[TK], nuv[TK], mx[8][2];
+  __shared__ int page[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int s = blockIdx.z, hl = blockIdx.y, h = a.head0 + hl;
+  const SeqSpan sp = paged_span(a.p, s);
+  if (sp.n == 0 || static_cast<int64_t>(blockIdx.x) * EX * TK >= sp.len) return;
+  if (tid < 16) {
+    ckt[tid] = a.books.ck[tid];
+    cvt[tid] = a.books.cv[tid];
+  }
+  if (a.books.qjl) {
+    // operand order: k-step ks, register r, half e of thread column t is
+    // coordinate 32 t + 2 ks + r + 16 e (d = 64: 16 t + 2 ks + r + 8 e) of the sketch
+    for (int e = tid; e < KS * NN * 32; e += 256) {
+      const int l = e & 31, nn = (e >> 5) % NN, ks = (e >> 5) / NN, j = 8 * nn + (l >> 2);
+      uint32_t w[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = (D == 128 ? 32 : 16) * (l & 3) + 2 * ks + r;
+        w[r] = a.S[i * D + j] | (static_cast<uint32_t>(a.S[(i + D / 8) * D + j]) << 16);
+      }
+      sfrag[e] = make_uint2(w[0], w[1]);
+    }
+  }
+  const int P = 1 << a.p.page_shift, mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
+  for (int tl = blockIdx.x * EX; tl < (blockIdx.x + 1) * EX && tl * TK < sp.len; ++tl) {
+    const int j0 = tl * TK;
+    uint8_t *img = a.tiles + ((static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles + tl) * tile_bytes(D);
+    __syncthreads();   // the last tile's scales have been read
+    if (tid < 4) page[tid] = j0 + 32 * tid < sp.len ? paged_page(a.p, s, j0 + 32 * tid) : -1;
+    __syncthreads();
+    // row of token j of the tile
+    auto row_of = [&](int j) {
+      return (static_cast<int64_t>(page[j >> 5]) * a.Hkv + h) * P + ((j0 + j) & (P - 1));
+    };
+    float nk = 0.f, rho = 0.f, nv = 0.f;
+    const bool there = tid < TK && page[(tid & (TK - 1)) >> 5] >= 0 && j0 + tid < sp.len;
+    if (there) {
+      const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row_of(tid)];
+      nk = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+      nv = tq_half_to_f32(a.vnorm[row_of(tid)]);
+    }
+    const uint32_t bits = __ballot_sync(TQ_FULL, there);
+    const float wk = tq_warp_max(nk), wv = tq_warp_max(nv);
+    if (lane == 0) {
+      mx[warp][0] = wk;
+      mx[warp][1] = wv;
+      if (warp < 4) reinterpret_cast<TileHeader *>(img)->there[warp] = bits;
+    }
+    __syncthreads();
+    float kmax = 0.f, vmax = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      kmax = fmaxf(kmax, mx[w][0]);
+      vmax = fmaxf(vmax, mx[w][1]);
+    }
+    const int ke = kmax > 0.f ? ilogbf(kmax) + 1 : 0, ve = vmax > 0.f ? ilogbf(vmax) + 1 : 0;
+    if (tid < TK) {
+      nuk[tid] = ldexpf(nk, -ke);
+      nuv[tid] = ldexpf(nv, -ve);
+    }
+    if (tid == 0) {
+      TileHeader *hd = reinterpret_cast<TileHeader *>(img);
+      hd->k_exp = ldexpf(1.f, ke);
+      hd->v_exp = static_cast<float>(ve);
+      hd->v_inv = ldexpf(1.f, -ve);
+      bool all = j0 + TK <= sp.len;
+      for (int i = 0; i < 4; ++i) all = all && page[i] >= 0;
+      hd->all = all;
+    }
+    __syncthreads();
+    // ---- keys: warp w takes tokens 16 w .. 16 w + 15
+    {
+      const int r0 = 16 * warp + g;
+      const bool on = page[warp >> 1] >= 0;
+      const int64_t base = on ? row_of(r0) : 0;
+      const uint32_t *kr0 = reinterpret_cast<const uint32_t *>(a.kcode + base * planes * (D / 8));
+      const uint32_t *kr1 = kr0 + 8 * planes * NPL;
+      const uint32_t *sc = reinterpret_cast<const uint32_t *>(a.kscale) + base;
+      float acc[NN][4];
+#pragma unroll
+      for (int n = 0; n < NN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+      float f0 = 0.f, f1 = 0.f;
+      if (a.books.qjl && on) {
+        uint32_t sg0 = kr0[mbk * NPL + (D == 128 ? t : t >> 1)], sg1 = kr1[mbk * NPL + (D == 128 ? t : t >> 1)];
+        if (D == 64) {
+          sg0 = prmt(sg0, 0u, t & 1 ? 0x4342 : 0x4140);
+          sg1 = prmt(sg1, 0u, t & 1 ? 0x4342 : 0x4140);
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t a0 = ((sg0 << (15 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
+          const uint32_t a1 = ((sg1 << (15 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
+          const uint32_t a2 = ((sg0 << (14 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
+          const uint32_t a3 = ((sg1 << (14 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
+#pragma unroll
+          for (int n = 0; n < NN; ++n) {
+            const uint2 b = sfrag[(ks * NN + n) * 32 + lane];
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                "{%0,%1,%2,%3};"
+                : "+f"(acc[n][0]), "+f"(acc[n][1]), "+f"(acc[n][2]), "+f"(acc[n][3])
+                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+          }
+        }
+        rho = tq_half_to_f32(static_cast<uint16_t>(sc[0] >> 16));
+        f0 = a.qjl_coef * rho;
+        f1 = a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc[8] >> 16));
+      }
+      const float n0 = nuk[r0], n1 = nuk[r0 + 8];
+      // rows past the end may hold anything: their factor is exactly zero
+      const bool e0 = n0 > 0.f, e1 = n1 > 0.f;
+      uint8_t *kimg = img + HDR;
+#pragma unroll
+      for (int w = 0; w < NPL; ++w) {
+        uint32_t p0[4], p1[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          p0[p] = on && p < mbk ? kr0[p * NPL + w] : 0u;
+          p1[p] = on && p < mbk ? kr1[p * NPL + w] : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = 4 * w + i, b = 8 * i + 2 * t;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            int i0 = 0, i1 = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              i0 |= ((p0[p] >> (b + e)) & 1u) << p;
+              i1 |= ((p1[p] >> (b + e)) & 1u) << p;
+            }
+            v[e] = e0 ? n0 * fmaf(f0, acc[n][e], ckt[i0]) : 0.f;
+            v[2 + e] = e1 ? n1 * fmaf(f1, acc[n][2 + e], ckt[i1]) : 0.f;
+          }
+          uint8_t *o = kimg + n * (TK * 16) + 2 * warp * 128 + g * 16 + t * 4;
+          *reinterpret_cast<uint32_t *>(o) = pack_half(v[0], v[1]);
+          *reinterpret_cast<uint32_t *>(o + 128) = pack_half(v[2], v[3]);
+        }
+      }
+    }
+    // ---- values, transposed: (coordinate, 32-token group) a thread
+    for (int it = tid; it < 4 * D; it += 256) {
+      const int c = it % D, gr = it / D;
+      const bool on = page[gr] >= 0;
+      uint32_t w[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        w[p] = on && p < nbv ? a.vcode[((row_of(32 * gr) >> 5) * nbv + p) * D + c] : 0u;
+      uint8_t *vimg = img + HDR + TK * D * 2 + (c >> 3) * 128 + (c & 7) * 16;
+#pragma unroll
+      for (int k8 = 0; k8 < 4; ++k8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2) {
+          float v[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int b = 8 * k8 + 2 * k2 + e;
+            int idx = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) idx |= ((w[p] >> b) & 1u) << p;
+            const float nu = nuv[32 * gr + b];
+            v[e] = nu > 0.f ? nu * cvt[idx] : 0.f;
+          }
+          o[k2] = pack_half(v[0], v[1]);
+        }
+        *reinterpret_cast<uint4 *>(vimg + (4 * gr + k8) * (D * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ attention
+
+template <int D>
+struct Smem {
+  static constexpr int STG = D == 128 ? 2 : 4;
+  static constexpr uint32_t OPER = TK * D * 2;   // one operand tile
+  static constexpr uint32_t Q = 0, K = 2 * OPER, V = K + STG * OPER, END = V + STG * OPER;
+};
+
+// Bounded wait that gives up as soon as another thread has.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint32_t outer, volatile int *abort_flag) {
+  for (uint32_t it = 0; it < outer; ++it) {
+    if (sm100::mbar_wait(bar, parity, 1u << 14)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  using L = Smem<D>;
+  constexpr int NPL = D / 32, STG = L::STG;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t kfull[STG], kempty[STG], vfull[STG], vempty[STG], sfull[2], pfull[2], ofull[2],
+      fin;
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  __shared__ float frow[2][TQ];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = a.units - 1 - static_cast<int>(blockIdx.x);   // the units with most keys first
+  const int hl = blockIdx.y, kvh = a.head0 + hl, split = blockIdx.z;
+  const int per = 2 * a.tok_tile;
+  const int s = paged_find_seq(a.p, unit, per, 1);
+  const SeqSpan sp = paged_span(a.p, s);
+  const int u = unit - paged_unit_base(a.p, s, per, 1);
+  const int tok0 = u * per;
+  if (u < 0 || tok0 >= sp.n) return;
+  const int pos0 = sp.len - sp.n;          // position of new token 0
+  // token tiles of the two query tiles, and of this block
+  int vis[2], k1[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int first = tok0 + x * a.tok_tile, last = min(first + a.tok_tile, sp.n) - 1;
+    vis[x] = first < sp.n ? max(0, min(sp.len, pos0 + last + 1)) : 0;
+    k1[x] = min((vis[x] + TK - 1) / TK, (split + 1) * a.chunk);
+  }
+  const int k0 = split * a.chunk;
+  const int nA = max(0, k1[0] - k0), nB = max(0, k1[1] - k0), n = max(nA, nB);
+  if (n == 0 && split > 0) return;
+
+  if (warp == 8) sm100::tmem_alloc(&tmem_s, 512);
+  if (tid == 0) {
+    for (int i = 0; i < STG; ++i) {
+      sm100::mbar_init(&kfull[i], 1);
+      sm100::mbar_init(&kempty[i], 1);
+      sm100::mbar_init(&vfull[i], 1);
+      sm100::mbar_init(&vempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&sfull[i], 1);
+      sm100::mbar_init(&pfull[i], TQ);
+      sm100::mbar_init(&ofull[i], 1);
+    }
+    sm100::mbar_init(&fin, 1);
+    abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  const uint8_t *img0 = a.tiles + (static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles * tile_bytes(D);
+  // ---- query operands: warp w of a tile's four prepares rows 32 w .. 32 w + 31
+  if (warp < 8) {
+    const int x = warp >> 2;
+    uint8_t *qimg = sm + L::Q + x * L::OPER;
+    for (int r = 32 * (warp & 3); r < 32 * (warp & 3) + 32; ++r) {
+      const int tt = r / a.G, tok = tok0 + x * a.tok_tile + tt, pos = pos0 + tok;
+      const bool on = tt < a.tok_tile && tok < sp.n && pos >= 0;
+      const int64_t off = static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + r % a.G) * a.sh;
+      float v[NPL];
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) v[k] = on ? tq_load_elem(a.q, off + lane + 32 * k, a.dtype) : 0.f;
+      if (a.rc != nullptr && on) {
+#pragma unroll
+        for (int k = 0; k < NPL / 2; ++k) {
+          const float c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
+          const float sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
+          const float p = v[k], w = v[k + NPL / 2];
+          v[k] = p * c - w * sn;
+          v[k + NPL / 2] = w * c + p * sn;
+        }
+      }
+      float f = a.scale * 1.4426950408889634f;
+      if (a.books.pi != nullptr) {
+        // the value operands' place holds no tile yet
+        tq_warp_dense<NPL>(v, a.books.pi_t, reinterpret_cast<float *>(sm + L::V) + warp * D, lane);
+      } else {
+        tq_apply_signs<NPL>(v, a.books.dneg, lane);
+        tq_warp_wht<NPL>(v, lane);
+        f *= 1.0f / sqrtf(static_cast<float>(D));
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        v[k] *= f;
+        m = fmaxf(m, fabsf(v[k]));
+      }
+      m = tq_warp_max(m);
+      // a power of two taken out where fp16 would lose digits or overflow
+      const int e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-120, min(120, ilogbf(m) + 1)) : 0;
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        const int c = lane + 32 * k;
+        *reinterpret_cast<__half *>(qimg + (c >> 3) * (TQ * 16) + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2) =
+            __float2half_rn(e == 0 ? v[k] : ldexpf(v[k], -e));
+      }
+      if (lane == 0) frow[x][r] = ldexpf(1.f, e);
+    }
+    sm100::fence_async_smem();
+  }
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  const uint32_t tm = tmem_s;
+
+  if (warp == 9) {
+    // ---- copies
+    if (lane == 0) {
+      int kc = 0, vc = 0;     // tiles copied so far
+      for (int i = 0; i < n; ++i) {
+        const int st = i % STG;
+        const uint8_t *img = img0 + static_cast<int64_t>(k0 + i) * tile_bytes(D);
+        if (i >= STG && !wait_for(&kempty[st], (i / STG - 1) & 1, a.wait_outer, &abort_s)) break;
+        sm100::mbar_expect_tx(&kfull[st], L::OPER);
+        sm100::bulk_g2s(sm + L::K + st * L::OPER, img + HDR, L::OPER, &kfull[st]);
+        ++kc;
+        if (i >= STG && !wait_for(&vempty[st], (i / STG - 1) & 1, a.wait_outer, &abort_s)) break;
+        sm100::mbar_expect_tx(&vfull[st], L::OPER);
+        sm100::bulk_g2s(sm + L::V + st * L::OPER, img + HDR + L::OPER, L::OPER, &vfull[st]);
+        ++vc;
+      }
+      // nothing may be in flight when the block's shared memory is released:
+      // the last copy of every slot has landed
+      for (int i = max(0, kc - STG); i < kc; ++i) sm100::mbar_wait(&kfull[i % STG], (i / STG) & 1, 1u << 24);
+      for (int i = max(0, vc - STG); i < vc; ++i) sm100::mbar_wait(&vfull[i % STG], (i / STG) & 1, 1u << 24);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---- products, issued by one thread
+    if (lane == 0) {
+      constexpr uint32_t ID_S = sm100::idesc_f16(TQ, TK), ID_O = sm100::idesc_f16(TQ, D);
+      const uint32_t aq = sm100::smem_addr(sm + L::Q), ak = sm100::smem_addr(sm + L::K),
+                     av = sm100::smem_addr(sm + L::V);
+      auto s_mma = [&](int x, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          sm100::mma_bf16_ss(tm + x * 128, sm100::smem_desc(aq + x * L::OPER + k * 2 * (TQ * 16), TQ * 16, 128),
+                             sm100::smem_desc(ak + st * L::OPER + k * 2 * (TK * 16), TK * 16, 128), ID_S,
+                             k > 0 ? 1u : 0u);
+      };
+      auto o_mma = [&](int x, int st, bool first) {
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k)
+          sm100::mma_f16_ts(tm + 256 + x * D, tm + x * 128 + k * 8,
+                            sm100::smem_desc(av + st * L::OPER + k * 2 * (D * 16), D * 16, 128), ID_O,
+                            (k > 0 || !first) ? 1u : 0u);
+      };
+      const int nx[2] = {nA, nB};
+      bool ok = n > 0 && wait_for(&kfull[0], 0, a.wait_outer, &abort_s);
+      if (ok) {
+        for (int x = 0; x < 2; ++x)
+          if (nx[x] > 0) {
+            s_mma(x, 0);
+            sm100::mma_commit(&sfull[x]);
+          }
+        sm100::mma_commit(&kempty[0]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i % STG, st1 = (i + 1) % STG;
+        if (i + 1 < n) ok = wait_for(&kfull[st1], ((i + 1) / STG) & 1, a.wait_outer, &abort_s);
+        ok = ok && wait_for(&vfull[st], (i / STG) & 1, a.wait_outer, &abort_s);
+        for (int x = 0; ok && x < 2; ++x) {
+          if (i >= nx[x]) continue;
+          ok = wait_for(&pfull[x], i & 1, a.wait_outer, &abort_s);
+          if (!ok) break;
+          sm100::fence_after_sync();
+          o_mma(x, st, i == 0);
+          if (i + 1 < nx[x]) {
+            s_mma(x, st1);
+            sm100::mma_commit(&sfull[x]);
+          } else {
+            sm100::mma_commit(&ofull[x]);
+          }
+        }
+        sm100::mma_commit(&vempty[st]);
+        if (i + 1 < n) sm100::mma_commit(&kempty[st1]);
+      }
+      // every product has landed before tensor memory is released
+      sm100::mma_commit(&fin);
+      sm100::mbar_wait(&fin, 0, 1u << 24);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: a thread a query row
+    const int x = warp >> 2, r = tid & (TQ - 1), lq = warp & 3;
+    const int tt = r / a.G, tok = tok0 + x * a.tok_tile + tt;
+    const bool live = tt < a.tok_tile && tok < sp.n;
+    const int pos = live ? pos0 + tok : -1;
+    const int pos_min = pos0 + tok0 + x * a.tok_tile;       // smallest of the tile
+    const float f = frow[x][r];
+    const int nx = x ? nB : nA;
+    const uint32_t tS = sm100::tmem_lane(tm + x * 128, lq), tO = sm100::tmem_lane(tm + 256 + x * D, lq);
+    float M = -1e30f, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nx; ++i) {
+      const TileHeader *hd =
+          reinterpret_cast<const TileHeader *>(img0 + static_cast<int64_t>(k0 + i) * tile_bytes(D));
+      const float F = hd->k_exp * f, ve = hd->v_exp, vi = hd->v_inv;
+      const int j0 = (k0 + i) * TK;
+      const bool masked = !hd->all || j0 + TK - 1 > pos_min;
+      ok = wait_for(&sfull[x], i & 1, a.wait_outer, &abort_s);
+      if (!__all_sync(TQ_FULL, ok)) break;
+      sm100::fence_after_sync();
+      uint32_t sv[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sm100::tmem_ld32(tS + 32 * c, sv[c]);
+      sm100::wait_ld();
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int lim = pos - (j0 + 32 * c);      // last visible of these 32
+          const uint32_t see = hd->there[c] & (lim < 0 ? 0u : lim >= 31 ? ~0u : (2u << lim) - 1u);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1u)) sv[c][e] = 0xff800000u;
+        }
+      }
+      float mx = -CUDART_INF_F;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[c][e]));
+      const float top = fmaf(mx, F, ve);
+      // the reference moves only when a weight would exceed 2^8
+      if (__any_sync(TQ_FULL, top > M + 8.f)) {
+        const float mn = fmaxf(M, top), corr = ex2(M - mn);
+        M = mn;
+        l *= corr;
+        if (i > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            sm100::tmem_ld32(tO + c, o);
+            sm100::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            sm100::tmem_st32(tO + c, o);
+          }
+        }
+      }
+      const float off = ve - M;
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pw[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = ex2(fmaf(__uint_as_float(sv[2 * c + (e >> 4)][(2 * e) & 31]), F, off));
+          const float p1 = ex2(fmaf(__uint_as_float(sv[2 * c + (e >> 4)][(2 * e + 1) & 31]), F, off));
+          sum += p0 + p1;
+          pw[e] = pack_half(p0, p1);
+        }
+        sm100::tmem_st32(tS + 32 * c, pw);
+      }
+      l = fmaf(sum, vi, l);
+      sm100::wait_st();
+      sm100::fence_before_sync();
+      sm100::mbar_arrive(&pfull[x]);
+    }
+    if (ok && nx > 0) ok = wait_for(&ofull[x], 0, a.wait_outer, &abort_s);
+    ok = __all_sync(TQ_FULL, ok);
+    sm100::fence_after_sync();
+    float o[D];
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      uint32_t w[32];
+      sm100::tmem_ld32(tO + c, w);
+      sm100::wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[c + e] = nx > 0 ? __uint_as_float(w[e]) : 0.f;
+    }
+    if (!ok) l = CUDART_NAN_F;    // a wait ran out: the rows are answered with NaN
+    const int64_t row = static_cast<int64_t>(sp.row0 + tok) * a.Hq + kvh * a.G + r % a.G;
+    // a split past the row's tiles writes nothing, and the join reads nothing
+    if (live && a.splits > 1 && (split == 0 || nx > 0)) {
+      float4 *dst = reinterpret_cast<float4 *>(a.po + (row * a.splits + split) * D);
+#pragma unroll
+      for (int c = 0; c < D; c += 4) dst[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      a.pml[row * a.splits + split] = make_float2(M, l);
+    } else if (live && a.splits == 1) {
+      const float inv = (l == 0.f ? 0.f : 1.0f / l) / sqrtf(static_cast<float>(D));
+#pragma unroll
+      for (int w = 1; w < D; w <<= 1)
+#pragma unroll
+        for (int c = 0; c < D; ++c)
+          if (!(c & w)) {
+            const float p = o[c], q = o[c + w];
+            o[c] = p + q;
+            o[c + w] = p - q;
+          }
+#pragma unroll
+      for (int c = 0; c < D; ++c) o[c] *= ((a.books.dneg[c >> 5] >> (c & 31)) & 1u) ? -inv : inv;
+      if (a.out_dtype == TQ_BF16) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D);
+#pragma unroll
+        for (int c = 0; c < D; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[c + 2 * e], o[c + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+          }
+          dst[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D);
+#pragma unroll
+        for (int c = 0; c < D; c += 4) dst[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      }
+    }
+    sm100::fence_before_sync();
+  }
+  __syncthreads();
+  sm100::fence_after_sync();
+  if (warp == 8) sm100::tmem_dealloc(tm, 512);
+}
+
+// The splits' sums of an answer row joined, rotated back, stored (a warp a row).
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int NPL = D / 32;
+  __shared__ float dsc[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+  const int hq = a.heads * a.G;
+  const int tok = static_cast<int>(it / hq), h = a.head0 * a.G + static_cast<int>(it % hq);
+  if (tok >= a.p.N) return;
+  const int s = paged_find_seq(a.p, tok, 1, 0);
+  const SeqSpan sp = paged_span(a.p, s);
+  const int i = tok - sp.row0;
+  if (i < 0 || i >= sp.n) return;
+  const int last = min((i / a.tok_tile + 1) * a.tok_tile, sp.n) - 1;      // of the row's query tile
+  const int vis = max(0, min(sp.len, sp.len - sp.n + last + 1));
+  const int n = max(1, ((vis + TK - 1) / TK + a.chunk - 1) / a.chunk);
+  const int64_t row = static_cast<int64_t>(tok) * a.Hq + h;
+  const float2 *ml = a.pml + row * a.splits;
+  float mx = -CUDART_INF_F;
+  for (int j = lane; j < n; j += 32) mx = fmaxf(mx, ml[j].x);
+  mx = tq_warp_max(mx);
+  float l = 0.f, x[NPL];
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const float2 m = ml[j];
+    const float f = ex2(m.x - mx);
+    l = fmaf(m.y, f, l);
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) x[k] = fmaf(a.po[(row * a.splits + j) * D + lane + 32 * k], f, x[k]);
+  }
+  paged_store_row<D>(x, l, a.books, dsc[warp], a.out, a.out_dtype, row, lane);
+}
+
+// ------------------------------------------------------------------ host
+
+struct Plan {
+  int tok_tile, units, max_tiles, splits, chunk, heads;   // heads: KV heads a pass
+  size_t tile_space, total;
+};
+
+constexpr size_t TILE_SPACE = size_t{1} << 30;   // of expanded tiles, unless one KV head needs more
+
+Plan plan(const tq_codec *c, int N, int num_seqs, int max_len, int Hq, int Hkv) {
+  Plan p;
+  const int G = Hq / Hkv;
+  p.tok_tile = TQ / G;
+  p.units = static_cast<int>(paged_units_bound(N, 2 * p.tok_tile, 1, num_seqs));
+  p.max_tiles = std::max(1, (max_len + TK - 1) / TK);
+  const size_t head = static_cast<size_t>(num_seqs) * p.max_tiles * tile_bytes(c->d);
+  p.heads = static_cast<int>(std::min<size_t>(Hkv, std::max<size_t>(1, TILE_SPACE / head)));
+  p.tile_space = head * p.heads;
+  // blocks walk the tiles of a query pair; with too few of them for the SMs
+  // the tiles are split (at least 4 a block) and the parts joined.  A dense
+  // rotation always takes the join, which rotates back row by row.
+  const int64_t blocks = std::max<int64_t>(1, static_cast<int64_t>(std::min<int64_t>(
+      p.units, (N + 2 * p.tok_tile - 1) / (2 * p.tok_tile) + num_seqs - 1)) * p.heads);
+  int64_t want = blocks >= 148 ? 1 : (148 + blocks - 1) / blocks;
+  want = std::min<int64_t>(want, std::max(1, p.max_tiles / 4));
+  if (c->rot_dev && want == 1) want = 2;
+  p.chunk = static_cast<int>((p.max_tiles + want - 1) / want);
+  p.splits = (p.max_tiles + p.chunk - 1) / p.chunk;
+  if (c->rot_dev && p.splits == 1) p.splits = 2;   // the second part is empty
+  p.total = p.tile_space;
+  if (p.splits > 1) p.total += static_cast<size_t>(N) * Hq * p.splits * (c->d + 2) * sizeof(float);
+  return p;
+}
+
+template <int D>
+int run_prefill(PrefillArgs &a, const Plan &pl, cudaStream_t stream) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool done[64] = {};
+  constexpr int shm = Smem<D>::END;
+  if (dev < 64 && !done[dev]) {
+    if (cudaFuncSetAttribute(paged_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, shm) != cudaSuccess)
+      return tq_check_launch("cudaFuncSetAttribute(paged_prefill)");
+    done[dev] = true;
+  }
+  const size_t es = a.books.qjl ? sizeof(uint2) * (D / 16) * (D / 8) * 32 : 0;
+  for (int h0 = 0; h0 < a.Hkv; h0 += pl.heads) {
+    a.head0 = h0;
+    a.heads = std::min(pl.heads, a.Hkv - h0);
+    const dim3 eg((pl.max_tiles + EX - 1) / EX, a.heads, a.p.num_seqs);
+    paged_expand_kernel<D><<<eg, 256, es, stream>>>(a);
+    if (int e = tq_check_launch("paged_expand_kernel")) return e;
+    paged_prefill_kernel<D><<<dim3(pl.units, a.heads, pl.splits), 320, shm, stream>>>(a);
+    if (int e = tq_check_launch("paged_prefill_kernel")) return e;
+    tq_count_launch(2);
+    if (pl.splits > 1) {
+      const int64_t rows = static_cast<int64_t>(a.p.N) * a.heads * a.G;
+      paged_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(a);
+      if (int e = tq_check_launch("paged_join_kernel")) return e;
+      tq_count_launch(1);
+    }
+  }
+  return TQ_OK;
+}
+
+}  // namespace
+
+size_t paged_prefill_workspace_bytes(const tq_codec *c, int N, int num_seqs, int max_len, int Hq, int Hkv) {
+  return plan(c, N, num_seqs, max_len, Hq, Hkv).total;
+}
+
+int launch_paged_prefill(const tq_codec *c, const PagedView &p, const void *q, int dtype, int64_t st, int64_t sh,
+                         int Hq, const tq_cache *cache, float scale, const float *rc, const float *rs, void *ws,
+                         void *out, int out_dtype, cudaStream_t stream) {
+  const Plan pl = plan(c, p.N, p.num_seqs, p.max_len, Hq, cache->Hkv);
+  PrefillArgs a;
+  a.p = p;
+  a.q = q;
+  a.dtype = dtype;
+  a.st = st;
+  a.sh = sh;
+  a.Hq = Hq;
+  a.Hkv = cache->Hkv;
+  a.G = Hq / cache->Hkv;
+  a.kcode = cache->kcode;
+  a.kscale = cache->kscale;
+  a.vcode = cache->vcode;
+  a.vnorm = cache->vnorm;
+  a.scale = scale;
+  a.qjl_coef = c->qjl_k ? sqrtf(static_cast<float>(M_PI) / 2.0f) / c->d : 0.f;
+  a.rc = rc;
+  a.rs = rs;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.S = c->S_dev;
+  a.tiles = static_cast<uint8_t *>(ws);
+  a.max_tiles = pl.max_tiles;
+  a.tok_tile = pl.tok_tile;
+  a.units = pl.units;
+  a.splits = pl.splits;
+  a.chunk = pl.chunk;
+  a.po = reinterpret_cast<float *>(a.tiles + pl.tile_space);
+  a.pml = reinterpret_cast<float2 *>(a.po + static_cast<size_t>(p.N) * Hq * pl.splits * c->d);
+  a.wait_outer = 1u << 12;
+  if (const char *e = getenv("TQ_WAIT_LIMIT"))
+    a.wait_outer = static_cast<uint32_t>((strtoul(e, nullptr, 10) + (1u << 14) - 1) >> 14);
+  a.books = c->books;
+  return c->d == 64 ? run_prefill<64>(a, pl, stream) : run_prefill<128>(a, pl, stream);
+}
