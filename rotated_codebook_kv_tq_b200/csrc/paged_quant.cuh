@@ -1,0 +1,205 @@
+// Arguments of the paged append kernels and the 64-bit coding of a row.
+#pragma once
+
+#include "paged.h"
+
+struct PagedQuantArgs {
+  PagedView p;
+  const void *k, *v;
+  int dtype;
+  int Hkv;
+  int64_t st, sh;
+  const float *rc, *rs;
+  uint8_t *kcode;
+  uint16_t *kscale;
+  uint32_t *vcode;
+  uint16_t *vnorm;
+  uint32_t *status;
+  const uint16_t *S;
+  int64_t units;          // tile kernels: (sequence, row tile) units, bound
+  uint32_t wait_limit;
+  TqBooks books;
+};
+
+// ------------------------------------------------------------------ 64 bits
+
+__device__ __forceinline__ double warp_sum_f64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(TQ_FULL, v, o);
+  return v;
+}
+
+// nu and u = Pi x / nu of a warp-held row (coordinate lane + 32 k), in 64
+// bits; a row with a non-finite element or an fp16-overflowing norm becomes
+// the zero row.  scratch: d doubles of this warp (dense rotations).
+template <int NPL>
+__device__ __noinline__ double unit_f64(double (&x)[NPL], const TqBooks &bk, double *scratch, int lane, bool &bad) {
+  constexpr int D = NPL * 32;
+  bool finite = true;
+  double ss = 0.0;
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) {
+    finite &= isfinite(x[k]);
+    ss += x[k] * x[k];
+  }
+  bad = __any_sync(TQ_FULL, !finite);
+  double nu = sqrt(warp_sum_f64(ss));
+  if (!bad && isinf(__half2float(__double2half(nu)))) bad = true;
+  if (bad) nu = 0.0;
+  const double inv = nu > 0.0 ? 1.0 / nu : 0.0;
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] = inv > 0.0 ? x[k] : 0.0;
+  if (bk.pi != nullptr) {
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) scratch[lane + 32 * k] = x[k];
+    __syncwarp();
+    double acc[NPL];
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) acc[k] = 0.0;
+    for (int j = 0; j < D; ++j)
+#pragma unroll
+      for (int k = 0; k < NPL; ++k)
+        acc[k] = fma(static_cast<double>(bk.pi_t[j * D + lane + 32 * k]), scratch[j], acc[k]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) x[k] = acc[k] * inv;
+    return nu;
+  }
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] = (bk.dneg[k] >> lane) & 1u ? -x[k] : x[k];
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) {
+      const double o = __shfl_xor_sync(TQ_FULL, x[k], s);
+      x[k] = lane & s ? o - x[k] : x[k] + o;
+    }
+#pragma unroll
+  for (int s = 1; s < NPL; s <<= 1)
+#pragma unroll
+    for (int k = 0; k < NPL; ++k)
+      if (!(k & s)) {
+        const double a = x[k], b = x[k + s];
+        x[k] = a + b;
+        x[k + s] = a - b;
+      }
+  const double f = inv / sqrt(static_cast<double>(D));
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] *= f;
+  return nu;
+}
+
+// A key row after RoPE, or a value row (pos < 0: no rotation), in 64 bits.
+template <int NPL>
+__device__ __forceinline__ void load_f64(double (&x)[NPL], const void *base, int64_t off, int dtype, const float *rc,
+                                         const float *rs, int64_t pos, int lane) {
+  constexpr int D = NPL * 32;
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(base, off + lane + 32 * k, dtype);
+  if (rc != nullptr) {
+#pragma unroll
+    for (int k = 0; k < NPL / 2; ++k) {
+      const double c = rc[pos * (D / 2) + lane + 32 * k], sn = rs[pos * (D / 2) + lane + 32 * k];
+      const double u = x[k], w = x[k + NPL / 2];
+      x[k] = u * c - w * sn;
+      x[k + NPL / 2] = w * c + u * sn;
+    }
+  }
+}
+
+__device__ __forceinline__ int code_f64(double u, const float *t) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < TQ_MAX_LEVELS - 1; ++i) n += u >= static_cast<double>(t[i]);
+  return n;
+}
+
+// Whole key row by one warp; whether the row was bad (coded as the zero row).
+// buf: d doubles of this warp.
+template <int D>
+__device__ __noinline__ bool key_row_f64(const PagedQuantArgs &a, int64_t off, int64_t pos, int64_t row, double *buf,
+                                         int lane) {
+  constexpr int NPL = D / 32;
+  const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
+  double x[NPL];
+  bool bad;
+  load_f64<NPL>(x, a.k, off, a.dtype, a.rc, a.rs, pos, lane);
+  const double nu = unit_f64<NPL>(x, a.books, buf, lane, bad);
+  uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + row * planes * (D / 8));
+  double r2 = 0.0;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) {
+    const int idx = code_f64(x[k], a.books.tk);
+    for (int p = 0; p < mbk; ++p) {
+      const uint32_t w = __ballot_sync(TQ_FULL, (idx >> p) & 1);
+      if (lane == 0) krow[p * NPL + k] = w;
+    }
+    const double r = x[k] - static_cast<double>(a.books.ck[idx]);
+    buf[lane + 32 * k] = r;
+    r2 += r * r;
+  }
+  double rho = 0.0;
+  if (a.books.qjl) {
+    rho = sqrt(warp_sum_f64(r2));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) {
+      const uint4 *sr = reinterpret_cast<const uint4 *>(a.S + (lane + 32 * k) * D);
+      double z = 0.0;
+#pragma unroll 4
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4 v = sr[j];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z = fma(static_cast<double>(__uint_as_float(w[e] << 16)), buf[8 * j + 2 * e], z);
+          z = fma(static_cast<double>(__uint_as_float(w[e] & 0xffff0000u)), buf[8 * j + 2 * e + 1], z);
+        }
+      }
+      const uint32_t w = __ballot_sync(TQ_FULL, z >= 0.0);
+      if (lane == 0) krow[mbk * NPL + k] = w;
+    }
+    __syncwarp();
+  }
+  if (lane == 0)
+    reinterpret_cast<uint32_t *>(a.kscale)[row] =
+        __half_as_ushort(__double2half(nu)) | (static_cast<uint32_t>(__half_as_ushort(__double2half(rho))) << 16);
+  return bad;
+}
+
+// Bits of one token in its group's column words.
+template <int D>
+__device__ __forceinline__ void store_value_bits(const PagedQuantArgs &a, int64_t row, const int (&idx)[D / 32],
+                                                 int lane) {
+  uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D;
+  const uint32_t bit = 1u << (row & 31);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k)
+    for (int p = 0; p < a.books.bits_v; ++p) {
+      uint32_t *w = vg + p * D + lane + 32 * k;
+      if ((idx[k] >> p) & 1)
+        atomicOr(w, bit);
+      else
+        atomicAnd(w, ~bit);
+    }
+}
+
+template <int D>
+__device__ __noinline__ bool value_row_f64(const PagedQuantArgs &a, int64_t off, int64_t row, double *buf, int lane) {
+  constexpr int NPL = D / 32;
+  double x[NPL];
+  bool bad;
+  load_f64<NPL>(x, a.v, off, a.dtype, nullptr, nullptr, 0, lane);
+  const double nu = unit_f64<NPL>(x, a.books, buf, lane, bad);
+  int idx[NPL];
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) idx[k] = code_f64(x[k], a.books.tv);
+  store_value_bits<D>(a, row, idx, lane);
+  if (lane == 0) a.vnorm[row] = __half_as_ushort(__double2half(nu));
+  return bad;
+}
+
+// Tiles of 128 cache rows on the tensor cores (paged_quantize_tile.cu).
+bool paged_quantize_tiles_fit(const tq_codec *c, const PagedQuantArgs &a);
+int launch_paged_quantize_tiles(const tq_codec *c, PagedQuantArgs &a, cudaStream_t stream);

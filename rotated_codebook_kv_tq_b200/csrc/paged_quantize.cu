@@ -2,192 +2,227 @@
 //
 // Same row computation as quantize.cu ("TurboESM ...", section 2.A: RoPE, then
 // the rotation; "FibQuant ...", section 2.3; "Google presenta TurboQuant ...",
-// "Eliminacion del sesgo"), with the codes of exact arithmetic: a coordinate's
-// code does not depend on the batch a token arrives in.
-#include "paged.h"
+// "Eliminacion del sesgo"), with the codes of exact arithmetic: rows are
+// coded in fp32, and a row with a coordinate nearer to a code border (or a sketch
+// value nearer to zero) than the fp32 computation can be off is coded again in
+// 64 bits.  A token's codes so depend neither on the batch it arrives in nor on the
+// kernel that takes it.
+//
+// Two kernels: one block a (token, head) for few rows and for what the other
+// does not take (dense rotations, unaligned rows); tiles of 128 cache rows with the
+// rotation and the sketch as tensor-core products for many.
+#include "paged_quant.cuh"
+#include "tq_sm100.cuh"
+
+#include <cstdlib>
 
 namespace {
 
-struct PagedQuantArgs {
-  PagedView p;
-  const void *k, *v;
-  int dtype;
-  int Hkv;
-  int64_t st, sh;
-  const float *rc, *rs;
-  uint8_t *kcode;
-  uint16_t *kscale;
-  uint32_t *vcode;
-  uint16_t *vnorm;
-  uint32_t *status;
-  const uint16_t *S;
-  TqBooks books;
-};
+// ------------------------------------------------------------------ few rows
 
-__device__ __forceinline__ double warp_sum_f64(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(TQ_FULL, v, o);
-  return v;
+// How far a computed u may be from the exact one: RoPE, norm, log2 d additions
+// and three products, each off by at most 2^-24 of sums that stay below the
+// row's norm (a dense rotation: d additions): 16 (d + 16) steps, doubled.
+template <int D>
+__device__ __forceinline__ float border_band(const TqBooks &bk) {
+  return bk.pi != nullptr ? (D + 16) * 1.2e-7f : 32 * 1.2e-7f;
 }
 
-// nu and u = Pi x / nu of a warp-held row (coordinate lane + 32 k), in 64
-// bits; a row with a non-finite element or an fp16-overflowing norm becomes
-// the zero row.  scratch: d doubles of this warp.
+// u = Pi x / nu in fp32 with everything that the 64-bit path would decide
+// differently flagged: `near` a border of t, or a norm outside fp32's safe range.
 template <int NPL>
-__device__ __forceinline__ double unit_f64(double (&x)[NPL], const TqBooks &bk, double *scratch,
-                                           int lane, bool &bad) {
-  constexpr int D = NPL * 32;
+__device__ __forceinline__ float unit_f32(float (&x)[NPL], const TqBooks &bk, float *scratch, int lane, bool &bad,
+                                          bool &again) {
   bool finite = true;
-  double ss = 0.0;
+  float ss = 0.f;
 #pragma unroll
   for (int k = 0; k < NPL; ++k) {
     finite &= isfinite(x[k]);
     ss += x[k] * x[k];
   }
   bad = __any_sync(TQ_FULL, !finite);
-  double nu = sqrt(warp_sum_f64(ss));
-  if (!bad && isinf(__half2float(__double2half(nu)))) bad = true;
-  if (bad) nu = 0.0;
-  const double inv = nu > 0.0 ? 1.0 / nu : 0.0;
+  ss = tq_warp_sum(ss);
+  again = !bad && (ss < 1e-24f || ss > 4.2e9f);     // norms below 1e-12, or near fp16's end
+  const float nu = bad ? 0.f : sqrtf(ss);
+  const float inv = nu > 0.f ? 1.0f / nu : 0.f;
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] = inv > 0.0 ? x[k] : 0.0;
-  if (bk.pi != nullptr) {
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) scratch[lane + 32 * k] = x[k];
-    __syncwarp();
-    double acc[NPL];
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) acc[k] = 0.0;
-    for (int j = 0; j < D; ++j)
-#pragma unroll
-      for (int k = 0; k < NPL; ++k)
-        acc[k] = fma(static_cast<double>(bk.pi_t[j * D + lane + 32 * k]), scratch[j], acc[k]);
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) x[k] = acc[k] * inv;
-    return nu;
+  for (int k = 0; k < NPL; ++k) x[k] = bad ? 0.f : x[k];
+  float f = inv;
+  if (bk.pi_t != nullptr) {
+    tq_warp_dense<NPL>(x, bk.pi_t, scratch, lane);
+  } else {
+    tq_apply_signs<NPL>(x, bk.dneg, lane);
+    tq_warp_wht<NPL, true>(x, lane);
+    f *= 1.0f / sqrtf(static_cast<float>(NPL * 32));
   }
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] = (bk.dneg[k] >> lane) & 1u ? -x[k] : x[k];
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      const double o = __shfl_xor_sync(TQ_FULL, x[k], s);
-      x[k] = lane & s ? o - x[k] : x[k] + o;
-    }
-#pragma unroll
-  for (int s = 1; s < NPL; s <<= 1)
-#pragma unroll
-    for (int k = 0; k < NPL; ++k)
-      if (!(k & s)) {
-        const double a = x[k], b = x[k + s];
-        x[k] = a + b;
-        x[k + s] = a - b;
-      }
-  const double f = inv / sqrt(static_cast<double>(D));
-#pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] *= f;
+  for (int k = 0; k < NPL; ++k) x[k] = nu > 0.f ? x[k] * f : 0.f;
   return nu;
 }
 
-__device__ __forceinline__ int code_f64(double u, const float *t) {
+// Code of u and its distance to the nearest threshold.
+__device__ __forceinline__ int code_f32(float u, const float *t, float &dist) {
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < TQ_MAX_LEVELS - 1; ++i) n += u >= static_cast<double>(t[i]);
+  for (int i = 0; i < TQ_MAX_LEVELS - 1; ++i) {
+    const float e = u - t[i];
+    n += e >= 0.f;
+    dist = fminf(dist, fabsf(e));
+  }
   return n;
 }
 
-// One warp per (new token, KV head).
 template <int D>
-__global__ void __launch_bounds__(128) paged_quantize_kernel(PagedQuantArgs a) {
+__global__ void __launch_bounds__(128) paged_quantize_kernel(const __grid_constant__ PagedQuantArgs a) {
   constexpr int NPL = D / 32;
-  __shared__ double buf[4][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + warp;
-  const int tok = static_cast<int>(it / a.Hkv), h = static_cast<int>(it % a.Hkv);
-  if (tok >= a.p.N) return;
+  __shared__ double buf[2][D];
+  __shared__ __align__(16) float rsm[D];
+  __shared__ float fscr[2][D], rho_s;
+  __shared__ uint32_t sgw[NPL];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok = static_cast<int>(blockIdx.x / a.Hkv), h = static_cast<int>(blockIdx.x % a.Hkv);
+  // row tid of S, loaded up front: its latency runs under the row's
+  uint4 srow[D / 8];
+  if (a.books.qjl && tid < D) {
+    const uint4 *sp = reinterpret_cast<const uint4 *>(a.S + tid * D);
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q) srow[q] = sp[q];
+  }
+  sm100::pdl_wait();
   const int s = paged_find_seq(a.p, tok, 1, 0);
   const SeqSpan sp = paged_span(a.p, s);
   const int i = tok - sp.row0, pos = sp.len - sp.n + i;
   if (i < 0 || i >= sp.n || pos < 0) return;
   const int page = paged_page(a.p, s, pos);
   if (page < 0) {
-    if (lane == 0 && a.status) atomicAdd(a.status, 2u);
+    if (tid == 0 && a.status) atomicAdd(a.status, 2u);
     return;
   }
   const int P = 1 << a.p.page_shift;
   const int64_t row = (static_cast<int64_t>(page) * a.Hkv + h) * P + (pos & (P - 1));
   const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
   const int64_t off = tok * a.st + h * a.sh;
-  double x[NPL];
-  bool bad;
-#pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(a.k, off + lane + 32 * k, a.dtype);
-  if (a.rc != nullptr) {
-#pragma unroll
-    for (int k = 0; k < NPL / 2; ++k) {
-      const double c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-      const double sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-      const double u = x[k], w = x[k + NPL / 2];
-      x[k] = u * c - w * sn;
-      x[k + NPL / 2] = w * c + u * sn;
-    }
-  }
-  const double nu = unit_f64<NPL>(x, a.books, buf[warp], lane, bad);
+  const float band = border_band<D>(a.books);
   uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + row * planes * (D / 8));
-  double r2 = 0.0;
+  sm100::pdl_trigger();
+  if (warp < 2) {
+    float x[NPL];
+    const void *src = warp == 0 ? a.k : a.v;
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    const int idx = code_f64(x[k], a.books.tk);
-    for (int p = 0; p < mbk; ++p) {
-      const uint32_t w = __ballot_sync(TQ_FULL, (idx >> p) & 1);
-      if (lane == 0) krow[p * NPL + k] = w;
+    for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(src, off + lane + 32 * k, a.dtype);
+    if (warp == 0 && a.rc != nullptr) {
+#pragma unroll
+      for (int k = 0; k < NPL / 2; ++k) {
+        const float c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
+        const float sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
+        const float u = x[k], w = x[k + NPL / 2];
+        x[k] = u * c - w * sn;
+        x[k + NPL / 2] = w * c + u * sn;
+      }
     }
-    const double r = x[k] - static_cast<double>(a.books.ck[idx]);
-    buf[warp][lane + 32 * k] = r;
-    r2 += r * r;
-  }
-  double rho = 0.0;
-  if (a.books.qjl) {
-    rho = sqrt(warp_sum_f64(r2));
-    __syncwarp();
+    bool bad, again;
+    float nu = unit_f32<NPL>(x, a.books, fscr[warp], lane, bad, again);
+    int idx[NPL];
+    float dist = 1.f;
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      double z = 0.0;
-      for (int j = 0; j < D; ++j)
-        z = fma(static_cast<double>(tq_bf16_to_f32(a.S[(lane + 32 * k) * D + j])), buf[warp][j], z);
-      const uint32_t w = __ballot_sync(TQ_FULL, z >= 0.0);
-      if (lane == 0) krow[mbk * NPL + k] = w;
+    for (int k = 0; k < NPL; ++k) idx[k] = code_f32(x[k], warp == 0 ? a.books.tk : a.books.tv, dist);
+    again |= nu > 0.f && __any_sync(TQ_FULL, dist < band);
+    float r[NPL];
+    if (again) {
+      double xd[NPL];
+      load_f64<NPL>(xd, src, off, a.dtype, warp == 0 ? a.rc : nullptr, a.rs, pos, lane);
+      nu = static_cast<float>(unit_f64<NPL>(xd, a.books, buf[warp], lane, bad));
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        idx[k] = code_f64(xd[k], warp == 0 ? a.books.tk : a.books.tv);
+        r[k] = static_cast<float>(xd[k] - static_cast<double>(a.books.ck[idx[k]]));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) r[k] = x[k] - a.books.ck[idx[k]];
     }
-    __syncwarp();
-  }
-  if (lane == 0) {
-    reinterpret_cast<uint32_t *>(a.kscale)[row] =
-        __half_as_ushort(__double2half(nu)) |
-        (static_cast<uint32_t>(__half_as_ushort(__double2half(rho))) << 16);
-    if (bad && a.status) atomicAdd(a.status, 1u);
-  }
+    if (bad && lane == 0 && a.status) atomicAdd(a.status, 1u);
+    if (warp == 0) {
+      uint32_t word = 0u;     // lane p * NPL + k stores word k of plane p
+      for (int p = 0; p < mbk; ++p)
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(a.v, off + lane + 32 * k, a.dtype);
-  const double nv = unit_f64<NPL>(x, a.books, buf[warp], lane, bad);
-  uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D;
-  const uint32_t bit = 1u << (pos & 31);
+        for (int k = 0; k < NPL; ++k) {
+          const uint32_t w = __ballot_sync(TQ_FULL, (idx[k] >> p) & 1);
+          if (lane == p * NPL + k) word = w;
+        }
+      if (lane < mbk * NPL) krow[lane] = word;
+      float r2 = 0.f;
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    const int idx = code_f64(x[k], a.books.tv);
-    for (int p = 0; p < a.books.bits_v; ++p) {
-      uint32_t *w = vg + p * D + lane + 32 * k;
-      if ((idx >> p) & 1)
-        atomicOr(w, bit);
-      else
-        atomicAnd(w, ~bit);
+      for (int k = 0; k < NPL; ++k) {
+        rsm[lane + 32 * k] = r[k];
+        r2 += r[k] * r[k];
+      }
+      const float rho = a.books.qjl ? sqrtf(tq_warp_sum(r2)) : 0.f;
+      if (lane == 0) {
+        rho_s = rho;
+        reinterpret_cast<uint32_t *>(a.kscale)[row] =
+            tq_f32_to_half(nu) | (static_cast<uint32_t>(tq_f32_to_half(rho)) << 16);
+      }
+    } else {
+      store_value_bits<D>(a, row, idx, lane);
+      if (lane == 0) a.vnorm[row] = tq_f32_to_half(nu);
     }
   }
-  if (lane == 0) {
-    a.vnorm[row] = __half_as_ushort(__double2half(nv));
-    if (bad && a.status) atomicAdd(a.status, 1u);
+  if (!a.books.qjl) return;
+  __syncthreads();
+  // z_i = <S_i, r>: eight partial sums of d / 8 products, so a step's error is
+  // at most (d / 8 + 4) 2^-24 of |S_i| |r|
+  float z = 0.f, ss = 0.f;
+  if (tid < D) {
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int q = 0; q < D / 8; ++q) {
+      const uint32_t w[4] = {srow[q].x, srow[q].y, srow[q].z, srow[q].w};
+      const float4 r0 = *reinterpret_cast<const float4 *>(rsm + 8 * q);
+      const float4 r1 = *reinterpret_cast<const float4 *>(rsm + 8 * q + 4);
+      const float rv[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+        acc[2 * e] = fmaf(lo, rv[2 * e], acc[2 * e]);
+        acc[2 * e + 1] = fmaf(hi, rv[2 * e + 1], acc[2 * e + 1]);
+        ss = fmaf(lo, lo, fmaf(hi, hi, ss));
+      }
+    }
+    z = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
   }
+  // the residual itself is off by up to the u it came from
+  const bool close = tid < D && !(fabsf(z) > sqrtf(ss) * ((D / 8 + 4) * 1.2e-7f * rho_s +
+                                                           4.f * sqrtf(static_cast<float>(D)) * 1.2e-7f));
+  if (__syncthreads_or(close)) {
+    if (warp == 0) {
+      double xd[NPL];
+      bool bad;
+      load_f64<NPL>(xd, a.k, off, a.dtype, a.rc, a.rs, pos, lane);
+      unit_f64<NPL>(xd, a.books, buf[1], lane, bad);
+#pragma unroll
+      for (int k = 0; k < NPL; ++k)
+        buf[0][lane + 32 * k] = xd[k] - static_cast<double>(a.books.ck[code_f64(xd[k], a.books.tk)]);
+    }
+    __syncthreads();
+    if (close) {
+      double zd = 0.0;
+#pragma unroll
+      for (int q = 0; q < D / 8; ++q) {
+        const uint32_t w[4] = {srow[q].x, srow[q].y, srow[q].z, srow[q].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          zd = fma(static_cast<double>(__uint_as_float(w[e] << 16)), buf[0][8 * q + 2 * e], zd);
+          zd = fma(static_cast<double>(__uint_as_float(w[e] & 0xffff0000u)), buf[0][8 * q + 2 * e + 1], zd);
+        }
+      }
+      z = zd >= 0.0 ? 1.f : -1.f;
+    }
+  }
+  const uint32_t sg = __ballot_sync(TQ_FULL, z >= 0.f);
+  if (lane == 0 && warp < NPL) krow[mbk * NPL + warp] = sg;
 }
 
 }  // namespace
@@ -213,11 +248,10 @@ int launch_paged_quantize(const tq_codec *c, const PagedView &p, const void *k, 
   a.S = c->S_dev;
   a.books = c->books;
   const int64_t rows = static_cast<int64_t>(p.N) * cache->Hkv;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (c->d == 64)
-    paged_quantize_kernel<64><<<grid, 128, 0, stream>>>(a);
-  else
-    paged_quantize_kernel<128><<<grid, 128, 0, stream>>>(a);
+  if (paged_quantize_tiles_fit(c, a)) return launch_paged_quantize_tiles(c, a, stream);
+  auto kern = c->d == 64 ? paged_quantize_kernel<64> : paged_quantize_kernel<128>;
+  if (tq_launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, a) != cudaSuccess)
+    return tq_check_launch("paged_quantize_kernel");
   tq_count_launch(1);
   return tq_check_launch("paged_quantize_kernel");
 }

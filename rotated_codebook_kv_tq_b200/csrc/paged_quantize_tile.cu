@@ -1,0 +1,797 @@
+// Append of many new tokens to a paged compressed cache: tiles of 128 cache
+// rows, the rotation and the sketch as tensor-core products.
+//
+// H_d diag(D) has entries +-1, exact in fp16, and a row scaled by a power of
+// two to a norm of 2^9 .. 2^10 is hi + lo of two fp16 terms to 2^-22 of an
+// element (a bf16 row is exact in one), so
+//   keys    y = X (H D)^T   rows in tensor-memory lanes, coordinates in columns
+//   values  y = (H D) X^T   coordinates in lanes, tokens in columns
+// come out of tcgen05.mma with fp32 accumulators as good as an fp32 transform, and
+// each side's threads find the bits of one output word in their own registers: 32
+// coordinates of a key row, 32 tokens of a value coordinate.  The key residual
+// goes back to tensor memory as hi + lo and is multiplied with S there.
+// Codes are decided on y against t_k sqrt(d) nu.  A row with a coordinate
+// within BAND of a threshold, or a sketch value within ZBAND |r| of zero, goes
+// on a list and is coded again in 64 bits, a warp a row.  The bands bound the
+// error: 2 d / 16 products are added one after another, each losing at most 2^-23
+// of a running sum below the row's norm.
+#include <cstdlib>
+
+#include "paged_quant.cuh"
+#include "tq_sm100.cuh"
+
+namespace {
+
+constexpr int TR = 128;             // cache rows of a tile
+constexpr int GT = 256;             // threads of a group (one tile); two groups a block
+constexpr int LIST = 512;           // rows to code again, per group
+constexpr float BAND = 2.5e-6f;     // of |u - t|
+constexpr float ZBAND = 2.5e-6f;    // of |z| / (max |S| |r|)
+
+struct FixRow {
+  int64_t row;
+  int tok, h, pos;
+};
+
+// Barrier of a group's 256 threads that tells whether all are on track.
+__device__ __forceinline__ bool group_ok(int id, bool ok) {
+  sm100::fence_before_sync();
+  uint32_t bad;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 q, %2, 0;\n\t"
+      "bar.red.or.pred p, %1, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(bad)
+      : "r"(id), "r"(ok ? 1u : 0u), "n"(GT)
+      : "memory");
+  sm100::fence_after_sync();
+  return bad == 0u;
+}
+
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+// (d0, d1) = (a0, a1) - c
+__device__ __forceinline__ void sub2(float a0, float a1, uint64_t c, float &d0, float &d1) {
+  asm("{\n\t.reg .b64 p, d;\n\tmov.b64 p, {%2, %3};\n\tsub.rn.f32x2 d, p, %4;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "l"(c));
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+
+// Eight values as the hi and lo fp16 terms of one 16-byte operand row each.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 a = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+    const float2 f = __half22float2(a);
+    h[e] = half2_bits(a);
+    l[e] = half2_bits(__floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Eight consecutive input elements.
+template <bool BF16>
+__device__ __forceinline__ void load8(float (&v)[8], const void *base, int64_t off) {
+  if (BF16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  } else {
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+__device__ __forceinline__ void load8f(float (&v)[8], const float *p) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Code words from the sign words of |y| - t_k (d[0..HK-2], ascending t_k > 0)
+// and of y (d[HK-1]) of 32 elements: an upper-half code counts the thresholds
+// passed, a lower-half one those not passed, so each plane is an XOR of the sign
+// words at which its bit flips.
+template <int NB>
+__device__ __forceinline__ void planes(const uint32_t (&d)[1 << (NB - 1)], uint32_t (&w)[NB]) {
+  constexpr int HK = 1 << (NB - 1);
+  const uint32_t sy = d[HK - 1];
+#pragma unroll
+  for (int p = 0; p < NB - 1; ++p) {
+    uint32_t x = sy;
+#pragma unroll
+    for (int k = (1 << p) - 1; k < HK - 1; k += 1 << p) x ^= d[k];
+    w[p] = ~x;
+  }
+  w[NB - 1] = ~sy;
+}
+
+// One tile of a group: sequence, first position, and what lies where.
+struct Tile {
+  int s, pos0, tile0, h;   // pos0: position of new token 0; tile0: first position of the tile
+  SeqSpan sp;
+  bool on;
+};
+
+__device__ __forceinline__ Tile find_tile(const PagedQuantArgs &a, int64_t unit) {
+  Tile t;
+  t.s = paged_find_seq(a.p, static_cast<int>(unit), TR, 2);
+  t.sp = paged_span(a.p, t.s);
+  t.pos0 = t.sp.len - t.sp.n;
+  const int lt = static_cast<int>(unit) - paged_unit_base(a.p, t.s, TR, 2);
+  t.tile0 = ((max(t.pos0, 0) >> 7) + lt) << 7;
+  t.on = lt >= 0 && t.sp.n > 0 && t.tile0 < t.sp.len;
+  return t;
+}
+
+// What a scaled row carries on.  e: power of two taken out, nu 2^-e in [2^9, 2^10).
+struct RowScale {
+  float nu, f;      // norm, 2^-e (0 for a zero row)
+  bool bad, again;
+};
+
+__device__ __forceinline__ RowScale row_scale(float ss, float amax) {
+  RowScale r;
+  r.bad = !(ss <= 4.3e9f);                      // not finite, or a norm beyond fp16 for sure
+  r.again = !r.bad && (ss > 4.2e9f || (ss < 1e-24f && amax > 0.f));
+  r.nu = r.bad ? 0.f : sqrtf(ss);
+  r.f = r.nu > 0.f ? ldexpf(1.f, 9 - ilogbf(r.nu)) : 0.f;
+  return r;
+}
+
+// H diag(D) as a K-major fp16 operand of R rows (block-diagonal for R = 128, d = 64).
+template <int D, int R>
+__device__ __forceinline__ void fill_rotation(uint8_t *dst, const TqBooks &bk, int tid, int nt) {
+  for (int e = tid; e < R * (R / 8); e += nt) {
+    const int i = e % R, c = e / R;          // row, 16-byte slice of eight inputs
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t hw[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int j = 8 * c + 2 * q + z;
+        const bool neg = (__popc((i % D) & (j % D)) + (bk.dneg[(j % D) >> 5] >> (j & 31))) & 1;
+        hw[z] = i / D != j / D ? 0u : neg ? 0xbc00u : 0x3c00u;
+      }
+      w[q] = hw[0] | (hw[1] << 16);
+    }
+    *reinterpret_cast<uint4 *>(dst + c * (R * 16) + (i >> 3) * 128 + (i & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ------------------------------------------------------------------ keys
+
+template <int D>
+constexpr size_t key_smem() { return 2 * D * D * 2 + 2 * 2 * TR * D * 2; }
+
+template <int D, int NB, bool QJL, bool BF16>
+__global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_constant__ PagedQuantArgs a) {
+  constexpr int HK = 1 << (NB - 1), LPR = D / 16, RPI = 32 / LPR, PL = NB + (QJL ? 1 : 0), NPL = D / 32;
+  constexpr uint32_t XB = TR * D * 2;                    // one operand term
+  constexpr uint32_t ID = sm100::idesc_f16(TR, D);
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ uint32_t tmem_s;
+  __shared__ int smax_s, nfix[2], abort_s;
+  __shared__ float rsc[2][TR], rnu[2][TR], r2s[2][2][TR];
+  __shared__ int rst[2][TR];           // 1: row of the call, 2: code again, 4: zero row
+  __shared__ int64_t rrow[2][TR];      // cache row
+  __shared__ FixRow fix[2][LIST];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = tid / GT, gt = tid % GT, wg = warp & 7;
+  uint8_t *hs = sm, *ss = sm + D * D * 2, *xs = ss + D * D * 2 + g * 2 * XB;
+  if (tid == 0) {
+    sm100::mbar_init(&bars[0], 1);
+    sm100::mbar_init(&bars[1], 1);
+    smax_s = 0;
+    nfix[0] = nfix[1] = 0;
+    abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) sm100::tmem_alloc(&tmem_s, 4 * D);
+  fill_rotation<D, D>(hs, a.books, tid, 2 * GT);
+  __syncthreads();
+  if (QJL) {
+    // S (bf16) in fp16: exact for entries of 2^-14 .. 2^16, off by 2^-25 below
+    float m = 0.f;
+    for (int e = tid; e < D * D / 8; e += 2 * GT) {
+      const int i = e % D, c = e / D;
+      const uint4 u = *reinterpret_cast<const uint4 *>(a.S + i * D + 8 * c);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float lo = __uint_as_float(w[q] << 16), hi = __uint_as_float(w[q] & 0xffff0000u);
+        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+        o[q] = half2_bits(__floats2half2_rn(lo, hi));
+      }
+      *reinterpret_cast<uint4 *>(ss + c * (D * 16) + (i >> 3) * 128 + (i & 7) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    atomicMax(&smax_s, __float_as_int(tq_warp_max(m)));
+  }
+  sm100::fence_async_smem();
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  sm100::pdl_wait();
+  const uint32_t tg = tmem_s + g * 2 * D;
+  const float zband = ZBAND * __int_as_float(smax_s) * (D / 128.f + 0.5f);
+  const int P = 1 << a.p.page_shift;
+  uint32_t ph = 0;
+  bool ok = true;
+  int committed = 0;
+  auto drain = [&]() {
+    double *buf = reinterpret_cast<double *>(xs) + wg * D;
+    for (int e = wg; e < nfix[g]; e += 8) {
+      const FixRow f = fix[g][e];
+      if (key_row_f64<D>(a, f.tok * a.st + f.h * a.sh, f.pos, f.row, buf, lane) && lane == 0 && a.status)
+        atomicAdd(a.status, 1u);
+    }
+  };
+  const int64_t total = a.units * a.Hkv;
+  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
+    Tile t = find_tile(a, w / a.Hkv);
+    t.h = static_cast<int>(w % a.Hkv);
+    if (!t.on) continue;
+    // ---- rows: LPR lanes a row, eight coordinates of each half a lane
+    const int j = lane % LPR;
+    float c0[16 / RPI][8], c1[16 / RPI][8];
+    int pos[16 / RPI];
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int r = 16 * wg + it * RPI + lane / LPR;
+      pos[it] = t.tile0 + r;
+      const int i = pos[it] - t.pos0;
+      const bool in = i >= 0 && i < t.sp.n;
+      if (in) {
+        const int64_t off = static_cast<int64_t>(t.sp.row0 + i) * a.st + t.h * a.sh + 8 * j;
+        load8<BF16>(c0[it], a.k, off);
+        load8<BF16>(c1[it], a.k, off + D / 2);
+      } else {
+        pos[it] = -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c0[it][e] = c1[it][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int r = 16 * wg + it * RPI + lane / LPR;
+      if (a.rc != nullptr && pos[it] >= 0) {
+        float cs[8], sn[8];
+        load8f(cs, a.rc + static_cast<int64_t>(pos[it]) * (D / 2) + 8 * j);
+        load8f(sn, a.rs + static_cast<int64_t>(pos[it]) * (D / 2) + 8 * j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = c0[it][e], v = c1[it][e];
+          c0[it][e] = u * cs[e] - v * sn[e];
+          c1[it][e] = v * cs[e] + u * sn[e];
+        }
+      }
+      float s2 = 0.f, mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s2 = fmaf(c0[it][e], c0[it][e], fmaf(c1[it][e], c1[it][e], s2));
+        mx = fmaxf(mx, fmaxf(fabsf(c0[it][e]), fabsf(c1[it][e])));
+      }
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) {
+        s2 += __shfl_xor_sync(TQ_FULL, s2, o);
+        mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+      }
+      const RowScale rs = row_scale(s2, mx);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c0[it][e] = rs.f > 0.f ? c0[it][e] * rs.f : 0.f;
+        c1[it][e] = rs.f > 0.f ? c1[it][e] * rs.f : 0.f;
+      }
+      uint4 hi, lo;
+      uint8_t *dst = xs + (r >> 3) * 128 + (r & 7) * 16;
+      split8(c0[it], hi, lo);
+      *reinterpret_cast<uint4 *>(dst + j * (TR * 16)) = hi;
+      *reinterpret_cast<uint4 *>(dst + XB + j * (TR * 16)) = lo;
+      split8(c1[it], hi, lo);
+      *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * (TR * 16)) = hi;
+      *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * (TR * 16)) = lo;
+      if (j == 0) {
+        int state = 0;
+        if (pos[it] >= 0) {
+          const int page = paged_page(a.p, t.s, pos[it]);
+          if (page >= 0) {
+            state = 1 | (rs.again ? 2 : 0) | (rs.nu > 0.f ? 0 : 4);
+            rrow[g][r] = (static_cast<int64_t>(page) * a.Hkv + t.h) * P + (pos[it] & (P - 1));
+            if (rs.bad && a.status) atomicAdd(a.status, 1u);
+          } else if (a.status) {
+            atomicAdd(a.status, 1u);
+          }
+        }
+        rst[g][r] = state;
+        rnu[g][r] = rs.nu;
+        rsc[g][r] = rs.nu > 0.f ? sqrtf(static_cast<float>(D)) * rs.nu * rs.f : 1.f;
+      }
+    }
+    sm100::fence_async_smem();
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (gt == 0) {
+#pragma unroll
+      for (int q = 0; q < 2 * D / 16; ++q) {
+        const int term = q / (D / 16), k = q % (D / 16);
+        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * (TR * 16), TR * 16, 128),
+                           sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (D * 16), D * 16, 128), ID, q > 0 ? 1u : 0u);
+      }
+      sm100::mma_commit(&bars[g]);
+      ++committed;
+    }
+    ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
+    ph ^= 1;
+    sm100::fence_after_sync();
+    // ---- codes: a thread a row and half of its coordinates
+    const int r = (wg & 3) * 32 + lane, hf = wg >> 2;
+    const uint32_t ty = sm100::tmem_lane(tg, wg & 3);
+    const int state = rst[g][r];
+    const float sc = rsc[g][r];
+    uint64_t th[HK];
+    float cen[HK];
+#pragma unroll
+    for (int k = 0; k < HK; ++k) {
+      if (k < HK - 1) th[k] = pk2(a.books.tk[HK + k] * sc, a.books.tk[HK + k] * sc);
+      cen[k] = a.books.ck[HK + k] * sc;
+    }
+    float dist = 1e30f, r2 = 0.f;
+    uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode) + (state & 1 ? rrow[g][r] : 0) * PL * NPL + hf * (NPL / 2);
+    const bool store = state & 1;
+#pragma unroll
+    for (int ch = 0; ch < NPL / 2; ++ch) {
+      uint32_t yv[32];
+      sm100::tmem_ld32(ty + hf * (D / 2) + 32 * ch, yv);
+      sm100::wait_ld();
+      if (state & 4) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) yv[e] = 0u;      // u = +0 decides the upper half
+      }
+      uint32_t dw[HK];
+#pragma unroll
+      for (int k = 0; k < HK; ++k) dw[k] = 0u;
+#pragma unroll
+      for (int e = 30; e >= 0; e -= 2) {
+        const float y0 = __uint_as_float(yv[e]), y1 = __uint_as_float(yv[e + 1]);
+        const float a0 = fabsf(y0), a1 = fabsf(y1);
+        float m0 = cen[0], m1 = cen[0];
+        dist = fminf(dist, fminf(a0, a1));
+#pragma unroll
+        for (int k = 0; k < HK - 1; ++k) {
+          float d0, d1;
+          sub2(a0, a1, th[k], d0, d1);
+          dw[k] = __funnelshift_l(__float_as_uint(d1), dw[k], 1);
+          dw[k] = __funnelshift_l(__float_as_uint(d0), dw[k], 1);
+          dist = fminf(dist, fminf(fabsf(d0), fabsf(d1)));
+          if (QJL) {
+            m0 = d0 >= 0.f ? cen[k + 1] : m0;
+            m1 = d1 >= 0.f ? cen[k + 1] : m1;
+          }
+        }
+        dw[HK - 1] = __funnelshift_l(yv[e + 1], dw[HK - 1], 1);
+        dw[HK - 1] = __funnelshift_l(yv[e], dw[HK - 1], 1);
+        if (QJL) {
+          const float r0 = a0 - m0, r1 = a1 - m1;
+          r2 = fmaf(r0, r0, fmaf(r1, r1, r2));
+          yv[e] = __float_as_uint(r0) ^ (yv[e] & 0x80000000u);
+          yv[e + 1] = __float_as_uint(r1) ^ (yv[e + 1] & 0x80000000u);
+        }
+      }
+      uint32_t pw[NB];
+      planes<NB>(dw, pw);
+      if (store) {
+#pragma unroll
+        for (int p = 0; p < NB; ++p) krow[p * NPL + ch] = pw[p];
+      }
+      if (QJL) {
+        // residual terms: tensor-memory columns d .. 3 d / 2 hi, 3 d / 2 .. 2 d lo
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v0 = __uint_as_float(yv[16 * q + 2 * e]), v1 = __uint_as_float(yv[16 * q + 2 * e + 1]);
+            const __half2 h2 = __floats2half2_rn(v0, v1);
+            const float2 f2 = __half22float2(h2);
+            hi[e] = half2_bits(h2);
+            lo[e] = half2_bits(__floats2half2_rn(v0 - f2.x, v1 - f2.y));
+          }
+          const uint32_t col = D + hf * (D / 4) + 16 * ch + 8 * q;
+          sm100::tmem_st8(ty + col, hi);
+          sm100::tmem_st8(ty + D / 2 + col, lo);
+        }
+      }
+    }
+    bool near = (state & 2) || (!(state & 4) && !(dist > BAND * sc));
+    float rho = 0.f;
+    if (QJL) {
+      sm100::wait_st();
+      r2s[g][hf][r] = r2;
+      if (!(ok = group_ok(1 + g, ok))) break;
+      if (gt == 0) {
+#pragma unroll
+        for (int q = 0; q < 2 * D / 16; ++q) {
+          const int term = q / (D / 16), k = q % (D / 16);
+          sm100::mma_f16_ts(tg, tg + D + term * (D / 2) + 8 * k,
+                            sm100::smem_desc(sm100::smem_addr(ss) + k * 2 * (D * 16), D * 16, 128), ID, q > 0 ? 1u : 0u);
+        }
+        sm100::mma_commit(&bars[g]);
+        ++committed;
+      }
+      ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
+      ph ^= 1;
+      sm100::fence_after_sync();
+      rho = sqrtf(r2s[g][0][r] + r2s[g][1][r]);
+      float zmin = 1e30f;
+#pragma unroll
+      for (int ch = 0; ch < NPL / 2; ++ch) {
+        uint32_t z[32], sg = 0u;
+        sm100::tmem_ld32(ty + hf * (D / 2) + 32 * ch, z);
+        sm100::wait_ld();
+#pragma unroll
+        for (int e = 31; e >= 0; --e) {
+          sg = __funnelshift_l(z[e], sg, 1);
+          zmin = fminf(zmin, fabsf(__uint_as_float(z[e])));
+        }
+        if (store) krow[NB * NPL + ch] = ~sg;
+      }
+      near |= !(zmin > zband * rho);
+    }
+    if (store && hf == 0)
+      reinterpret_cast<uint32_t *>(a.kscale)[rrow[g][r]] =
+          tq_f32_to_half(rnu[g][r]) | (static_cast<uint32_t>(tq_f32_to_half(rho / sc)) << 16);
+    if (store && near && !(atomicOr(&rst[g][r], 8) & 8)) {
+      FixRow f;
+      f.row = rrow[g][r];
+      f.pos = t.tile0 + r;
+      f.tok = t.sp.row0 + f.pos - t.pos0;
+      f.h = t.h;
+      fix[g][atomicAdd(&nfix[g], 1)] = f;
+    }
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (nfix[g] > LIST - TR) {
+      drain();
+      group_ok(1 + g, true);
+      if (gt == 0) nfix[g] = 0;
+      group_ok(1 + g, true);
+    }
+  }
+  sm100::pdl_trigger();
+  if (ok) {
+    drain();
+  } else {
+    abort_s = 1;
+  }
+  // this group's products have landed before tensor memory is released
+  if (gt == 0 && committed > 0) sm100::mbar_wait(&bars[g], (committed - 1) & 1, 1u << 24);
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  if (abort_s && tid == 0 && a.status) atomicOr(a.status, 1u << 31);
+  if (warp == 0) sm100::tmem_dealloc(tmem_s, 4 * D);
+}
+
+// ------------------------------------------------------------------ values
+
+template <bool BF16>
+constexpr size_t value_smem() { return 128 * 128 * 2 + 2 * (BF16 ? 1 : 2) * TR * 128 * 2; }
+
+// A tile's product has 128 lanes: the coordinates of one head (d = 128) or of two
+// (d = 64).
+template <int D, int NB, bool BF16>
+__global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_constant__ PagedQuantArgs a) {
+  constexpr int HK = 1 << (NB - 1), NH = 128 / D, LPR = D / 16, RPI = 32 / LPR, TERMS = BF16 ? 1 : 2;
+  constexpr uint32_t XB = TR * 128 * 2;
+  constexpr uint32_t ID = sm100::idesc_f16(128, TR);
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ uint32_t tmem_s;
+  __shared__ int nfix[2], abort_s;
+  __shared__ __align__(16) float rinv[2][NH][TR];    // 1 / (sqrt(d) nu 2^-e), 0 for a zero row
+  __shared__ uint32_t act[2][TR / 32], near[2][NH][TR / 32], zero[2][NH][TR / 32];
+  __shared__ int64_t grow[2][TR / 32];               // cache row of a 32-token group, head 0
+  __shared__ FixRow fix[2][LIST];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = tid / GT, gt = tid % GT, wg = warp & 7;
+  uint8_t *hs = sm, *xs = sm + 128 * 128 * 2 + g * TERMS * XB;
+  if (tid == 0) {
+    sm100::mbar_init(&bars[0], 1);
+    sm100::mbar_init(&bars[1], 1);
+    nfix[0] = nfix[1] = 0;
+    abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) sm100::tmem_alloc(&tmem_s, 256);
+  fill_rotation<D, 128>(hs, a.books, tid, 2 * GT);
+  sm100::fence_async_smem();
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  sm100::pdl_wait();
+  const uint32_t tg = tmem_s + g * 128;
+  const int P = 1 << a.p.page_shift;
+  uint32_t ph = 0;
+  bool ok = true;
+  int committed = 0;
+  auto drain = [&]() {
+    double *buf = reinterpret_cast<double *>(xs) + wg * D;
+    for (int e = wg; e < nfix[g]; e += 8) {
+      const FixRow f = fix[g][e];
+      if (value_row_f64<D>(a, f.tok * a.st + f.h * a.sh, f.row, buf, lane) && lane == 0 && a.status)
+        atomicAdd(a.status, 1u);
+    }
+  };
+  const int hgroups = (a.Hkv + NH - 1) / NH;
+  const int64_t total = a.units * hgroups;
+  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
+    Tile t = find_tile(a, w / hgroups);
+    t.h = static_cast<int>(w % hgroups) * NH;
+    if (!t.on) continue;
+    if (gt < TR) {
+      // which rows the call brings, a warp a 32-token group
+      const int pos = t.tile0 + gt, i = pos - t.pos0, p32 = t.tile0 + (gt & ~31);
+      const bool in = i >= 0 && i < t.sp.n;
+      const uint32_t any = __ballot_sync(TQ_FULL, in);
+      int page = -1;
+      if (any) page = paged_page(a.p, t.s, p32);
+      if (lane == 0) {
+        act[g][wg] = page >= 0 ? any : 0u;
+        grow[g][wg] = (static_cast<int64_t>(page) * a.Hkv + t.h) * P + (p32 & (P - 1));
+        if (page < 0 && any && a.status) atomicAdd(a.status, __popc(any) * min(NH, a.Hkv - t.h));
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh) near[g][hh][wg] = zero[g][hh][wg] = 0u;
+      }
+    }
+    if (!(ok = group_ok(1 + g, ok))) break;
+    const int j = lane % LPR;
+#pragma unroll
+    for (int hh = 0; hh < NH; ++hh) {
+      const bool head = t.h + hh < a.Hkv;
+      float c0[16 / RPI][8], c1[16 / RPI][8];
+#pragma unroll
+      for (int it = 0; it < 16 / RPI; ++it) {
+        const int r = 16 * wg + it * RPI + lane / LPR, i = t.tile0 + r - t.pos0;
+        if (head && ((act[g][r >> 5] >> (r & 31)) & 1u)) {
+          const int64_t off = static_cast<int64_t>(t.sp.row0 + i) * a.st + (t.h + hh) * a.sh + 8 * j;
+          load8<BF16>(c0[it], a.v, off);
+          load8<BF16>(c1[it], a.v, off + D / 2);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c0[it][e] = c1[it][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 16 / RPI; ++it) {
+        const int r = 16 * wg + it * RPI + lane / LPR;
+        float s2 = 0.f, mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s2 = fmaf(c0[it][e], c0[it][e], fmaf(c1[it][e], c1[it][e], s2));
+          mx = fmaxf(mx, fmaxf(fabsf(c0[it][e]), fabsf(c1[it][e])));
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) {
+          s2 += __shfl_xor_sync(TQ_FULL, s2, o);
+          mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+        }
+        const RowScale rs = row_scale(s2, mx);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c0[it][e] = rs.f > 0.f ? c0[it][e] * rs.f : 0.f;
+          c1[it][e] = rs.f > 0.f ? c1[it][e] * rs.f : 0.f;
+        }
+        uint4 hi, lo;
+        uint8_t *dst = xs + hh * (D / 8) * (TR * 16) + (r >> 3) * 128 + (r & 7) * 16;
+        split8(c0[it], hi, lo);
+        *reinterpret_cast<uint4 *>(dst + j * (TR * 16)) = hi;
+        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + j * (TR * 16)) = lo;
+        split8(c1[it], hi, lo);
+        *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * (TR * 16)) = hi;
+        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * (TR * 16)) = lo;
+        if (j == 0) {
+          rinv[g][hh][r] = rs.nu > 0.f ? 1.0f / (sqrtf(static_cast<float>(D)) * rs.nu * rs.f) : 0.f;
+          if (head && ((act[g][r >> 5] >> (r & 31)) & 1u)) {
+            a.vnorm[grow[g][r >> 5] + static_cast<int64_t>(hh) * P + (r & 31)] = tq_f32_to_half(rs.nu);
+            if (rs.bad && a.status) atomicAdd(a.status, 1u);
+            if (rs.again) atomicOr(&near[g][hh][r >> 5], 1u << (r & 31));
+            if (!(rs.nu > 0.f)) atomicOr(&zero[g][hh][r >> 5], 1u << (r & 31));
+          }
+        }
+      }
+    }
+    sm100::fence_async_smem();
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (gt == 0) {
+#pragma unroll
+      for (int q = 0; q < TERMS * 8; ++q) {
+        const int term = q / 8, k = q % 8;
+        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (128 * 16), 128 * 16, 128),
+                           sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * (TR * 16), TR * 16, 128), ID,
+                           q > 0 ? 1u : 0u);
+      }
+      sm100::mma_commit(&bars[g]);
+      ++committed;
+    }
+    ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
+    ph ^= 1;
+    sm100::fence_after_sync();
+    // ---- codes: a thread a coordinate and half of the tokens, 32 at a time
+    const int lq = wg & 3, hf = wg >> 2, hh = D == 128 ? 0 : lq >> 1, c = (lq * 32 + lane) % D;
+    uint64_t th[HK];
+#pragma unroll
+    for (int k = 0; k < HK - 1; ++k) th[k] = pk2(a.books.tv[HK + k], a.books.tv[HK + k]);
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      const int gr = 2 * hf + ch;                 // 32-token group
+      uint32_t yv[32];
+      sm100::tmem_ld32(sm100::tmem_lane(tg, lq) + 32 * gr, yv);
+      sm100::wait_ld();
+      const uint32_t on = act[g][gr];
+      if (on == 0u || t.h + hh >= a.Hkv) continue;
+      uint32_t dw[HK];
+      float dist = 1e30f;
+#pragma unroll
+      for (int k = 0; k < HK; ++k) dw[k] = 0u;
+#pragma unroll
+      for (int e4 = 28; e4 >= 0; e4 -= 4) {
+        const float4 iv = *reinterpret_cast<const float4 *>(&rinv[g][hh][32 * gr + e4]);
+        const float fi[4] = {iv.x, iv.y, iv.z, iv.w};
+#pragma unroll
+        for (int e2 = 2; e2 >= 0; e2 -= 2) {
+          const int e = e4 + e2;
+          const float u0 = __uint_as_float(yv[e]) * fi[e2], u1 = __uint_as_float(yv[e + 1]) * fi[e2 + 1];
+          yv[e] = __float_as_uint(u0);
+          yv[e + 1] = __float_as_uint(u1);
+          const float a0 = fabsf(u0), a1 = fabsf(u1);
+          dist = fminf(dist, fminf(a0, a1));
+#pragma unroll
+          for (int k = 0; k < HK - 1; ++k) {
+            float d0, d1;
+            sub2(a0, a1, th[k], d0, d1);
+            dw[k] = __funnelshift_l(__float_as_uint(d1), dw[k], 1);
+            dw[k] = __funnelshift_l(__float_as_uint(d0), dw[k], 1);
+            dist = fminf(dist, fminf(fabsf(d0), fabsf(d1)));
+          }
+          dw[HK - 1] = __funnelshift_l(yv[e + 1], dw[HK - 1], 1);
+          dw[HK - 1] = __funnelshift_l(yv[e], dw[HK - 1], 1);
+        }
+      }
+      // a zero row's u is +0 whatever sign the sum left
+      dw[HK - 1] &= ~zero[g][hh][gr];
+      uint32_t pw[NB];
+      planes<NB>(dw, pw);
+      const int64_t row = grow[g][gr] + static_cast<int64_t>(hh) * P;
+      uint32_t *vg = a.vcode + (row >> 5) * NB * D + c;
+#pragma unroll
+      for (int p = 0; p < NB; ++p) vg[p * D] = on == TQ_FULL ? pw[p] : (vg[p * D] & ~on) | (pw[p] & on);
+      if (__any_sync(TQ_FULL, !(dist > BAND))) {
+        uint32_t nb = 0u;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float av = fabsf(__uint_as_float(yv[e]));
+          float m = av;
+#pragma unroll
+          for (int k = 0; k < HK - 1; ++k) m = fminf(m, fabsf(av - a.books.tv[HK + k]));
+          nb |= !(m > BAND) ? 1u << e : 0u;
+        }
+        nb = __reduce_or_sync(TQ_FULL, nb & ~zero[g][hh][gr]);
+        if (lane == 0 && nb) atomicOr(&near[g][hh][gr], nb);
+      }
+    }
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (gt < NH * TR) {
+      const int r = gt % TR, nh = gt / TR;
+      if (((near[g][nh][r >> 5] & act[g][r >> 5]) >> (r & 31)) & 1u) {
+        FixRow f;
+        f.row = grow[g][r >> 5] + static_cast<int64_t>(nh) * P + (r & 31);
+        f.pos = t.tile0 + r;
+        f.tok = t.sp.row0 + f.pos - t.pos0;
+        f.h = t.h + nh;
+        const int at = atomicAdd(&nfix[g], 1);
+        if (at < LIST) fix[g][at] = f;
+      }
+    }
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (nfix[g] > LIST - NH * TR) {
+      drain();
+      group_ok(1 + g, true);
+      if (gt == 0) nfix[g] = 0;
+      group_ok(1 + g, true);
+    }
+  }
+  sm100::pdl_trigger();
+  if (ok) {
+    drain();
+  } else {
+    abort_s = 1;
+  }
+  if (gt == 0 && committed > 0) sm100::mbar_wait(&bars[g], (committed - 1) & 1, 1u << 24);
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  if (abort_s && tid == 0 && a.status) atomicOr(a.status, 1u << 31);
+  if (warp == 0) sm100::tmem_dealloc(tmem_s, 256);
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename K>
+int run_tiles(K kern, const char *name, size_t shm, int64_t tiles, const PagedQuantArgs &a, cudaStream_t stream) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm)) != cudaSuccess)
+    return tq_check_launch("cudaFuncSetAttribute(paged quantize tiles)");
+  const int grid = static_cast<int>(std::min<int64_t>(sms, (tiles + 1) / 2));
+  if (tq_launch_pdl(kern, dim3(grid), dim3(2 * GT), shm, stream, a) != cudaSuccess) return tq_check_launch(name);
+  tq_count_launch(1);
+  return tq_check_launch(name);
+}
+
+template <int D, int NB, bool QJL>
+int run_keys(const PagedQuantArgs &a, cudaStream_t stream) {
+  const int64_t tiles = a.units * a.Hkv;
+  return a.dtype == TQ_BF16
+             ? run_tiles(paged_qkey_kernel<D, NB, QJL, true>, "paged_qkey_kernel", key_smem<D>(), tiles, a, stream)
+             : run_tiles(paged_qkey_kernel<D, NB, QJL, false>, "paged_qkey_kernel", key_smem<D>(), tiles, a, stream);
+}
+
+template <int D, int NB>
+int run_values(const PagedQuantArgs &a, cudaStream_t stream) {
+  const int64_t tiles = a.units * ((a.Hkv + 128 / D - 1) / (128 / D));
+  return a.dtype == TQ_BF16
+             ? run_tiles(paged_qvalue_kernel<D, NB, true>, "paged_qvalue_kernel", value_smem<true>(), tiles, a, stream)
+             : run_tiles(paged_qvalue_kernel<D, NB, false>, "paged_qvalue_kernel", value_smem<false>(), tiles, a, stream);
+}
+
+template <int D, bool QJL>
+int run_keys_nb(int nb, const PagedQuantArgs &a, cudaStream_t stream) {
+  switch (nb) {
+    case 1: return run_keys<D, 1, QJL>(a, stream);
+    case 2: return run_keys<D, 2, QJL>(a, stream);
+    case 3: return run_keys<D, 3, QJL>(a, stream);
+    default: return run_keys<D, 4, QJL>(a, stream);
+  }
+}
+
+template <int D>
+int run_both(const tq_codec *c, const PagedQuantArgs &a, cudaStream_t stream) {
+  if (int e = c->qjl_k ? run_keys_nb<D, true>(c->mse_bits_k, a, stream) : run_keys_nb<D, false>(c->mse_bits_k, a, stream))
+    return e;
+  switch (c->bits_v) {
+    case 1: return run_values<D, 1>(a, stream);
+    case 2: return run_values<D, 2>(a, stream);
+    case 3: return run_values<D, 3>(a, stream);
+    default: return run_values<D, 4>(a, stream);
+  }
+}
+
+}  // namespace
+
+bool paged_quantize_tiles_fit(const tq_codec *c, const PagedQuantArgs &a) {
+  const int64_t es = a.dtype == TQ_BF16 ? 2 : 4;
+  const auto al = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (c->rot_dev || !al(a.k) || !al(a.v) || (a.st * es) % 16 || (a.sh * es) % 16 || !al(a.rc) || !al(a.rs)) return false;
+  // rows of 128 pay once the tiles are mostly full and there are enough of them
+  return a.p.N >= 32LL * a.p.num_seqs && static_cast<int64_t>(a.p.N) * a.Hkv >= 4096;
+}
+
+int launch_paged_quantize_tiles(const tq_codec *c, PagedQuantArgs &a, cudaStream_t stream) {
+  a.units = paged_units_bound(a.p.N, TR, 2, a.p.num_seqs);
+  a.wait_limit = 1u << 26;
+  if (const char *e = getenv("TQ_WAIT_LIMIT")) a.wait_limit = static_cast<uint32_t>(strtoul(e, nullptr, 10));
+  return c->d == 64 ? run_both<64>(c, a, stream) : run_both<128>(c, a, stream);
+}

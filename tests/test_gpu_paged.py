@@ -72,6 +72,15 @@ APPEND = [
     (64, 3, True, 2, 2, 32, [(40, 40), (1, 1)], "bf16", False, True),
     (128, 4, True, 4, 8, 64, [(1024, 1024), (700, 699)], "bf16", True, False),
     (64, 3, True, 3, 5, 32, [(900, 900), (801, 800)], "bf16", True, False),
+    (128, 5, True, 1, 4, 64, [(700, 600), (500, 500)], "fp32", True, False),
+    (128, 2, True, 2, 8, 32, [(513, 513), (70, 69)], "bf16", False, False),
+    (128, 3, False, 3, 6, 128, [(1000, 900)], "fp32", False, False),
+    (128, 4, False, 2, 6, 32, [(800, 790)], "bf16", True, False),
+    (64, 2, True, 4, 3, 64, [(1500, 1400), (129, 128)], "fp32", True, False),
+    (64, 1, False, 1, 6, 32, [(800, 799)], "bf16", True, False),
+    (64, 5, True, 2, 6, 32, [(800, 799)], "bf16", False, False),
+    (64, 4, False, 3, 7, 64, [(640, 600)], "fp32", True, False),
+    (128, 4, True, 4, 8, 32, [(33, 33)] * 17, "bf16", True, False),
 ]
 
 
@@ -162,6 +171,48 @@ def test_append_of_bad_rows_missing_pages_and_short_sequences():
     same_planes(cache, ref)
     lost = sum(1 for _, s, p in batch.rows() if p >= 0 and batch.page_of(s, p) is None)
     assert int(status.item()) == 3 + 2 * Hkv * lost
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp32")])
+def test_append_of_bad_rows_in_a_large_call(d, dtype):
+    """Rows that are zero, tiny, huge, not finite or on a border, missing pages, and
+    a sequence with more new tokens than tokens, in a call of full tiles."""
+    Hkv, page = 5, 64
+    ocodec, ncodec = pt.codecs(d, 4, True, 4)
+    batch = pt.Batch([(700, 600), (300, 320), (90, 90)], page, seed=4, start=1, extra_rows=1)
+    batch.table[0, 3] = batch.pool
+    batch.table[2, 0] = -1
+    planes = pt.random_pages(ocodec, batch.pool, Hkv, page)
+    cache = pt.upload(planes, ncodec)
+    kv, _ = make_kv(batch, Hkv, d, dtype)
+    r0 = int(batch.q_start[1])
+    kv[r0 + 30, 0, 5] = float("nan")
+    kv[r0 + 31, Hkv + 3, 0] = float("inf")
+    kv[r0 + 32, 1] *= 1e6                     # norm beyond fp16
+    kv[r0 + 33, :] = 0.0
+    kv[r0 + 34, :] = -0.0
+    kv[r0 + 35, :] *= 1e-14
+    kv[r0 + 36, :] *= 1e-30
+    kv[r0 + 37, :] = 1.0                      # one coordinate carries the row
+    kv[r0 + 38, :] = 0.0
+    kv[r0 + 38, :, 3] = -2.0                  # all coordinates equal in size
+    for i, e in enumerate((65503.0, 65504.0, 65519.0, 65521.0, 66000.0)):
+        kv[r0 + 40 + i, :] = 0.0
+        kv[r0 + 40 + i, :, 1] = e             # norms around fp16's end
+    kvh = host(kv)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.paged_quantize_kv(ncodec, kv[:, :Hkv], kv[:, Hkv:], cache, batch.device(), status=status)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = encode_ref(planes, ocodec, batch, kvh[:, :Hkv], kvh[:, Hkv:], None)
+    same_planes(cache, ref)
+    norm = np.sqrt((kvh * kvh).sum(-1))
+    with np.errstate(over="ignore", invalid="ignore"):
+        bad = ~np.isfinite(norm.astype(np.float16))
+    count = 0
+    for r, s, p in batch.rows():
+        if p >= 0:
+            count += 2 * Hkv if batch.page_of(s, p) is None else int(bad[r].sum())
+    assert int(status.item()) == count
 
 
 def test_append_does_not_depend_on_the_chunks():
