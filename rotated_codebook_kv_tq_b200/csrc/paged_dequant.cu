@@ -1,8 +1,14 @@
 // Rows of a paged compressed cache read back as vectors ("FibQuant ...",
 // section 2.3, decoder; keys add the QJL term):
-//   keys   nu Pi^T (c_k[idx] + sqrt(pi/2)/d rho S^T (2 sigma - 1))
+//   keys   nu Pi^T (c_k[idx] + coef rho S^T (2 sigma - 1)),  coef = sqrt(pi/2)/d
 //   values nu Pi^T c_v[idx]
-#include "paged.h"
+// Two kernels: a warp a row in fp32 (few rows, fp32 answers, dense rotations), and
+// tiles of 128 rows whose rotation and sketch are tensor-core products (bf16
+// answers of many rows).
+#include <cstdlib>
+
+#include "paged_expand.cuh"
+#include "tq_sm100.cuh"
 
 namespace {
 
@@ -17,18 +23,26 @@ struct PagedDequantArgs {
   int out_dtype;
   float qjl_coef;
   const uint16_t *S;
+  int64_t units;
+  uint32_t wait_limit;
+  uint32_t lutk[4], lutv[4];
   TqBooks books;
 };
 
-// One warp per (token, KV head).
+// ------------------------------------------------------------------ a warp a row
+
+// Block: the key warp and the value warp of a (token, KV head).
 template <int D>
-__global__ void __launch_bounds__(256) paged_dequant_kernel(PagedDequantArgs a) {
+__global__ void __launch_bounds__(64) paged_dequant_kernel(const __grid_constant__ PagedDequantArgs a) {
   constexpr int NPL = D / 32;
-  __shared__ float dsc[8][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  __shared__ float dsc[2][D];
+  __shared__ float acc_s[D];
+  const int lane = threadIdx.x & 31, which = threadIdx.x >> 5;
+  const int64_t it = blockIdx.x;
   const int tok = static_cast<int>(it / a.Hkv), h = static_cast<int>(it % a.Hkv);
-  if (tok >= a.p.N) return;
+  void *out = which ? a.v_out : a.k_out;
+  if (out == nullptr) return;
+  sm100::pdl_wait();
   const int s = paged_find_seq(a.p, tok, 1, 0);
   const SeqSpan sp = paged_span(a.p, s);
   const int i = tok - sp.row0, pos = sp.len - sp.n + i;
@@ -37,59 +51,337 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(PagedDequantArgs a) 
   const int P = 1 << a.p.page_shift;
   const int64_t row = (static_cast<int64_t>(page) * a.Hkv + h) * P + (pos & (P - 1));
   const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
-  for (int which = 0; which < 2; ++which) {
-    void *out = which ? a.v_out : a.k_out;
-    if (out == nullptr) continue;
-    float y[NPL], nu = 0.f;
+  float y[NPL], nu = 0.f;
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) y[k] = 0.f;
-    if (page >= 0 && which == 0) {
-      const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.kcode + row * planes * (D / 8));
-      const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row];
-      nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
-      if (a.books.qjl) {
-        for (int j = 0; j < D; ++j) {
-          const bool pos_sign = (krow[mbk * NPL + (j >> 5)] >> (j & 31)) & 1;
+  for (int k = 0; k < NPL; ++k) y[k] = 0.f;
+  if (page >= 0 && which == 0) {
+    const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.kcode + row * planes * (D / 8));
+    const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row];
+    nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+    if (a.books.qjl) {
+      // lane: columns NPL lane .. of S, one row of S a step
+      float z[NPL];
 #pragma unroll
-          for (int k = 0; k < NPL; ++k) {
-            const float sv = tq_bf16_to_f32(a.S[j * D + lane + 32 * k]);
-            y[k] += pos_sign ? sv : -sv;
+      for (int k = 0; k < NPL; ++k) z[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NPL; ++w) {
+        const uint32_t sg = krow[mbk * NPL + w];
+        const uint16_t *sr = a.S + w * 32 * D + NPL * lane;
+#pragma unroll 16
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t neg = (~(sg >> j) & 1u) << 31;
+          uint32_t v[NPL / 2];
+          if (NPL == 4) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(sr + j * D);
+            v[0] = u.x;
+            v[NPL / 2 - 1] = u.y;
+          } else {
+            v[0] = *reinterpret_cast<const uint32_t *>(sr + j * D);
+          }
+#pragma unroll
+          for (int k = 0; k < NPL / 2; ++k) {
+            z[2 * k] += __uint_as_float((v[k] << 16) ^ neg);
+            z[2 * k + 1] += __uint_as_float((v[k] & 0xffff0000u) ^ neg);
           }
         }
       }
-      const float f = a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) {
-        int idx = 0;
-        for (int p = 0; p < mbk; ++p) idx |= ((krow[p * NPL + k] >> lane) & 1) << p;
-        y[k] = fmaf(f, y[k], a.books.ck[idx]);
-      }
-    } else if (page >= 0) {
-      const uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D;
-      nu = tq_half_to_f32(a.vnorm[row]);
+      for (int k = 0; k < NPL; ++k) acc_s[NPL * lane + k] = z[k];
+      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) {
-        int idx = 0;
-        for (int p = 0; p < a.books.bits_v; ++p) idx |= ((vg[p * D + lane + 32 * k] >> (pos & 31)) & 1) << p;
-        y[k] = a.books.cv[idx];
-      }
+      for (int k = 0; k < NPL; ++k) y[k] = acc_s[lane + 32 * k];
     }
-    if (a.books.pi != nullptr) {
-      tq_warp_dense<NPL>(y, a.books.pi, dsc[warp], lane);
-    } else {
-      tq_warp_wht<NPL>(y, lane);
-      tq_apply_signs<NPL>(y, a.books.dneg, lane);
-      nu *= 1.0f / sqrtf(static_cast<float>(D));
-    }
+    const float f = a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
 #pragma unroll
     for (int k = 0; k < NPL; ++k) {
-      const int64_t o = it * D + lane + 32 * k;
-      if (a.out_dtype == TQ_BF16)
-        static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(y[k] * nu);
-      else
-        static_cast<float *>(out)[o] = y[k] * nu;
+      int idx = 0;
+      for (int p = 0; p < mbk; ++p) idx |= ((krow[p * NPL + k] >> lane) & 1) << p;
+      y[k] = fmaf(f, y[k], a.books.ck[idx]);
+    }
+  } else if (page >= 0) {
+    const uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D;
+    nu = tq_half_to_f32(a.vnorm[row]);
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) {
+      int idx = 0;
+      for (int p = 0; p < a.books.bits_v; ++p) idx |= ((vg[p * D + lane + 32 * k] >> (pos & 31)) & 1) << p;
+      y[k] = a.books.cv[idx];
     }
   }
+  if (a.books.pi != nullptr) {
+    tq_warp_dense<NPL>(y, a.books.pi, dsc[which], lane);
+  } else {
+    tq_warp_wht<NPL>(y, lane);
+    tq_apply_signs<NPL>(y, a.books.dneg, lane);
+    nu *= 1.0f / sqrtf(static_cast<float>(D));
+  }
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) {
+    const int64_t o = it * D + lane + 32 * k;
+    if (a.out_dtype == TQ_BF16)
+      static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(y[k] * nu);
+    else
+      static_cast<float *>(out)[o] = y[k] * nu;
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+
+constexpr int TR = 128;     // rows of a tile
+constexpr int GT = 256;     // threads of a group (one tile); two groups a block
+
+__device__ __forceinline__ bool group_ok(int id, bool ok) {
+  sm100::fence_before_sync();
+  uint32_t bad;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.eq.u32 q, %2, 0;\n\t"
+      "bar.red.or.pred p, %1, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(bad)
+      : "r"(id), "r"(ok ? 1u : 0u), "n"(GT)
+      : "memory");
+  sm100::fence_after_sync();
+  return bad == 0u;
+}
+
+// 32 x 32 bit transpose across a warp: bit L of lane i's result is bit i of
+// lane L's word.
+__device__ __forceinline__ uint32_t warp_transpose(uint32_t x, int lane) {
+  constexpr uint32_t masks[5] = {0xffff0000u, 0xff00ff00u, 0xf0f0f0f0u, 0xccccccccu, 0xaaaaaaaau};
+#pragma unroll
+  for (int st = 0; st < 5; ++st) {
+    const int j = 16 >> st;
+    const uint32_t y = __shfl_xor_sync(TQ_FULL, x, j);
+    const uint32_t r = rotr(y, lane & j ? j : 32 - j);
+    x = lane & j ? pick(masks[st], x, r) : pick(~masks[st], x, r);
+  }
+  return x;
+}
+
+// The 32 table entries of a row's plane words as 16 operand columns.  Column
+// 4 s + i holds coordinates 8 i + s and 8 i + 4 + s of the word.
+template <bool FOUR>
+__device__ __forceinline__ void expand32(uint32_t (&w)[4], const uint32_t (&lut)[4], uint32_t *o) {
+  if (FOUR) fold_sign(w);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    uint32_t q[4];
+    expand8<FOUR>(nibbles<FOUR>(w, s), lut, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[4 * s + i] = q[i];
+  }
+}
+
+template <int D>
+constexpr size_t tile_smem() { return 2 * D * D * 2; }
+
+// A tile is 128 cache rows of one (sequence, KV head), keys or values.  Its
+// expanded rows are the tensor-memory operand (lane = token, two coordinates a
+// column), D_c = +-1 and the sketch seen from the unrotated side, S Pi, the shared
+// memory operands:  answer = nu / sqrt(d) (c H D + (+-coef rho) (S H D)).
+// Operands are fp16 (centroids, coef rho, S H D: 2^-11 each), sums fp32.
+template <int D, bool K4, bool V4>
+__global__ void __launch_bounds__(2 * GT, 1) paged_dequant_tile_kernel(const __grid_constant__ PagedDequantArgs a) {
+  constexpr int NPL = D / 32;
+  constexpr uint32_t ID = sm100::idesc_f16(TR, D);
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ uint32_t tmem_s;
+  __shared__ int abort_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = tid / GT, gt = tid % GT, wg = warp & 7;
+  uint8_t *hs = sm, *ts = sm + D * D * 2;
+  if (tid == 0) {
+    sm100::mbar_init(&bars[0], 1);
+    sm100::mbar_init(&bars[1], 1);
+    abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) sm100::tmem_alloc(&tmem_s, 4 * D);
+  // rows: answer coordinates; K: coordinates in expand32's order
+  for (int e = tid; e < D * (D / 8); e += 2 * GT) {
+    const int j = e % D, c = e / D;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t hw[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int k = 8 * c + 2 * q + z, i = (k & ~31) + 4 * (k & 7) + ((k >> 3) & 3);
+        hw[z] = (__popc(i & j) + (a.books.dneg[j >> 5] >> (j & 31))) & 1 ? 0xbc00u : 0x3c00u;
+      }
+      w[q] = hw[0] | (hw[1] << 16);
+    }
+    *reinterpret_cast<uint4 *>(hs + c * (D * 16) + (j >> 3) * 128 + (j & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (a.books.qjl) {
+    // sketch rows rotated back; K: column x of a word holds coordinates x and x + 16
+    for (int i = warp; i < D; i += 16) {
+      float x[NPL];
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) x[k] = tq_bf16_to_f32(a.S[i * D + lane + 32 * k]);
+      tq_warp_wht<NPL>(x, lane);
+      tq_apply_signs<NPL>(x, a.books.dneg, lane);
+      const int kk = (i & ~31) + 2 * (i & 15) + ((i >> 4) & 1);
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        const int j = lane + 32 * k;
+        *reinterpret_cast<__half *>(ts + (kk >> 3) * (D * 16) + (j >> 3) * 128 + (j & 7) * 16 + (kk & 7) * 2) =
+            __float2half_rn(x[k]);
+      }
+    }
+  }
+  sm100::fence_async_smem();
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  sm100::pdl_wait();
+  const uint32_t tg = tmem_s + g * 2 * D;       // operand: D columns, sums: D columns
+  const int P = 1 << a.p.page_shift, mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
+  const int sides = (a.k_out != nullptr) + (a.v_out != nullptr);
+  const int lq = wg & 3, hf = wg >> 2, r = lq * 32 + lane;
+  const uint32_t tl = sm100::tmem_lane(tg, lq);
+  uint32_t ph = 0;
+  bool ok = true;
+  int committed = 0;
+  const int64_t total = a.units * a.Hkv * sides;
+  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
+    const bool vals = sides == 2 ? w & 1 : a.v_out != nullptr;
+    const int64_t q = w / sides;
+    const int unit = static_cast<int>(q / a.Hkv), h = static_cast<int>(q % a.Hkv);
+    const int s = paged_find_seq(a.p, unit, TR, 2);
+    const SeqSpan sp = paged_span(a.p, s);
+    const int pos0 = sp.len - sp.n, lt = unit - paged_unit_base(a.p, s, TR, 2);
+    const int tile0 = ((max(pos0, 0) >> 7) + lt) << 7;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(vals ? a.v_out : a.k_out);
+    if (lt < 0) continue;
+    if (lt == 0 && pos0 < 0) {
+      // new tokens without a position
+      for (int64_t e = gt; e < static_cast<int64_t>(min(-pos0, sp.n)) * (D / 8); e += GT)
+        *reinterpret_cast<uint4 *>(out + ((sp.row0 + e / (D / 8)) * a.Hkv + h) * D + 8 * (e % (D / 8))) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (sp.n == 0 || tile0 >= sp.len) continue;
+    const int pos = tile0 + r, i = pos - pos0;
+    const bool in = i >= 0 && i < sp.n;
+    const bool any = __any_sync(TQ_FULL, in);
+    const int page = any ? paged_page(a.p, s, tile0 + 32 * lq) : -1;
+    const int64_t row32 = (static_cast<int64_t>(page) * a.Hkv + h) * P + ((tile0 + 32 * lq) & (P - 1));
+    float f = 0.f;
+    if (page >= 0) {
+      uint32_t o[32];
+      if (!vals) {
+        const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row32 + lane];
+        const uint32_t *kr =
+            reinterpret_cast<const uint32_t *>(a.kcode + (row32 + lane) * planes * (D / 8)) + hf * (NPL / 2);
+        if (in) f = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+#pragma unroll
+        for (int x = 0; x < NPL / 2; ++x) {
+          uint32_t pw[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) pw[p] = p < mbk ? kr[p * NPL + x] : 0u;
+          expand32<K4>(pw, a.lutk, o + 16 * x);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 8)
+          sm100::tmem_st8(tl + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
+        if (a.books.qjl) {
+          const float rho = in ? tq_half_to_f32(static_cast<uint16_t>(sc >> 16)) : 0.f;
+          const uint32_t one = __half_as_ushort(__float2half_rn(a.qjl_coef * rho)) * 0x00010001u;
+#pragma unroll
+          for (int x = 0; x < NPL / 2; ++x) {
+            const uint32_t sg = ~kr[mbk * NPL + x];
+#pragma unroll
+            for (int b = 0; b < 16; ++b) o[16 * x + b] = ((sg << (15 - b)) & 0x80008000u) ^ one;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 4; c += 8)
+            sm100::tmem_st8(tl + D / 2 + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
+        }
+      } else {
+        const uint32_t *vg = a.vcode + (row32 >> 5) * nbv * D + hf * (D / 2);
+        if (in) f = tq_half_to_f32(a.vnorm[row32 + lane]);
+#pragma unroll
+        for (int x = 0; x < NPL / 2; ++x) {
+          uint32_t pw[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) pw[p] = p < nbv ? warp_transpose(vg[p * D + 32 * x + lane], lane) : 0u;
+          expand32<V4>(pw, a.lutv, o + 16 * x);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 8)
+          sm100::tmem_st8(tl + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
+      }
+      sm100::wait_st();
+    }
+    if (!(ok = group_ok(1 + g, ok))) break;
+    if (gt == 0) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        sm100::mma_f16_ts(tg + D, tg + 8 * k, sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (D * 16), D * 16, 128),
+                          ID, k > 0 ? 1u : 0u);
+      if (!vals && a.books.qjl) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          sm100::mma_f16_ts(tg + D, tg + D / 2 + 8 * k,
+                            sm100::smem_desc(sm100::smem_addr(ts) + k * 2 * (D * 16), D * 16, 128), ID, 1u);
+      }
+      sm100::mma_commit(&bars[g]);
+      ++committed;
+    }
+    ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
+    ph ^= 1;
+    sm100::fence_after_sync();
+    f *= 1.0f / sqrtf(static_cast<float>(D));
+    if (!__all_sync(TQ_FULL, ok)) f = __int_as_float(0x7fc00000);   // a wait ran out: NaN
+    uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(sp.row0 + i) * a.Hkv + h) * D + hf * (D / 2));
+#pragma unroll
+    for (int x = 0; x < NPL / 2; ++x) {
+      uint32_t v[32];
+      sm100::tmem_ld32(tl + D + hf * (D / 2) + 32 * x, v);
+      sm100::wait_ld();
+      if (in) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v0 = __uint_as_float(v[8 * c + 2 * e]), v1 = __uint_as_float(v[8 * c + 2 * e + 1]);
+            const __nv_bfloat162 t = __floats2bfloat162_rn(f == 0.f ? 0.f : v0 * f, f == 0.f ? 0.f : v1 * f);
+            b[e] = *reinterpret_cast<const uint32_t *>(&t);
+          }
+          dst[4 * x + c] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+      }
+    }
+  }
+  if (!ok) abort_s = 1;
+  if (gt == 0 && committed > 0) sm100::mbar_wait(&bars[g], (committed - 1) & 1, 1u << 24);
+  sm100::fence_before_sync();
+  __syncthreads();
+  sm100::fence_after_sync();
+  if (warp == 0) sm100::tmem_dealloc(tmem_s, 4 * D);
+}
+
+template <int D, bool K4, bool V4>
+int run_tiles(const PagedDequantArgs &a, cudaStream_t stream) {
+  auto kern = paged_dequant_tile_kernel<D, K4, V4>;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  constexpr size_t shm = tile_smem<D>();
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm)) != cudaSuccess)
+    return tq_check_launch("cudaFuncSetAttribute(paged_dequant_tile)");
+  const int64_t tiles = a.units * a.Hkv * ((a.k_out != nullptr) + (a.v_out != nullptr));
+  const int grid = static_cast<int>(std::min<int64_t>(sms, (tiles + 1) / 2));
+  if (tq_launch_pdl(kern, dim3(grid), dim3(2 * GT), shm, stream, a) != cudaSuccess)
+    return tq_check_launch("paged_dequant_tile_kernel");
+  tq_count_launch(1);
+  return tq_check_launch("paged_dequant_tile_kernel");
+}
+
+template <int D>
+int run_tiles_d(const PagedDequantArgs &a, bool k4, bool v4, cudaStream_t stream) {
+  if (k4) return v4 ? run_tiles<D, true, true>(a, stream) : run_tiles<D, true, false>(a, stream);
+  return v4 ? run_tiles<D, false, true>(a, stream) : run_tiles<D, false, false>(a, stream);
 }
 
 }  // namespace
@@ -108,13 +400,21 @@ int launch_paged_dequant(const tq_codec *c, const PagedView &p, const tq_cache *
   a.out_dtype = out_dtype;
   a.qjl_coef = c->qjl_k ? sqrtf(static_cast<float>(M_PI) / 2.0f) / c->d : 0.f;
   a.S = c->S_dev;
+  a.units = paged_units_bound(p.N, TR, 2, p.num_seqs);
+  a.wait_limit = 1u << 26;
+  if (const char *e = getenv("TQ_WAIT_LIMIT")) a.wait_limit = static_cast<uint32_t>(strtoul(e, nullptr, 10));
+  byte_table(c->books.ck, c->mse_bits_k, a.lutk);
+  byte_table(c->books.cv, c->bits_v, a.lutv);
   a.books = c->books;
   const int64_t rows = static_cast<int64_t>(p.N) * cache->Hkv;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (c->d == 64)
-    paged_dequant_kernel<64><<<grid, 256, 0, stream>>>(a);
-  else
-    paged_dequant_kernel<128><<<grid, 256, 0, stream>>>(a);
+  // tiles pay once they are mostly full and there are enough of them
+  if (out_dtype == TQ_BF16 && !c->rot_dev && p.N >= 32LL * p.num_seqs && rows >= 4096) {
+    const bool k4 = c->mse_bits_k == 4, v4 = c->bits_v == 4;
+    return c->d == 64 ? run_tiles_d<64>(a, k4, v4, stream) : run_tiles_d<128>(a, k4, v4, stream);
+  }
+  auto kern = c->d == 64 ? paged_dequant_kernel<64> : paged_dequant_kernel<128>;
+  if (tq_launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(64), 0, stream, a) != cudaSuccess)
+    return tq_check_launch("paged_dequant_kernel");
   tq_count_launch(1);
   return tq_check_launch("paged_dequant_kernel");
 }

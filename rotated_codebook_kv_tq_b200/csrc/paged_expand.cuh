@@ -1,0 +1,70 @@
+// Code planes to fp16 table entries by byte permutes, and the rotation operand.
+#pragma once
+
+#include <cstring>
+
+#include "paged.h"
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t rotr(uint32_t x, int n) { return __funnelshift_r(x, x, n); }
+
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) { return (a & m) | (b & ~m); }
+
+// Nibble words: nibble e of the result holds the code bits of element 4 e + s
+// of the plane words w[0..3].  With four planes the top one is the sign:
+// entries are looked up by magnitude (fold_sign), bit 3 of the nibble set
+// where the entry is negative.
+template <bool FOUR>
+__device__ __forceinline__ uint32_t nibbles(const uint32_t (&w)[4], int s) {
+  const uint32_t a = rotr(w[0], s), b = rotr(w[1], s + 31), c = rotr(w[2], s + 30);
+  uint32_t n = pick(0x11111111u, a, b);
+  n = pick(0x44444444u, c, n);
+  if (FOUR) return pick(0x88888888u, rotr(w[3], s + 29), n);
+  return n & 0x77777777u;
+}
+
+// Four code planes of an odd-symmetric codebook -> magnitude index planes
+// (0 the smallest) and the plane of negative signs.
+__device__ __forceinline__ void fold_sign(uint32_t (&w)[4]) {
+  w[3] = ~w[3];
+  w[0] ^= w[3];
+  w[1] ^= w[3];
+  w[2] ^= w[3];
+}
+
+// Eight fp16 table entries of a nibble word as four pairs (0,1) (2,3) (4,5) (6,7).
+template <bool FOUR>
+__device__ __forceinline__ void expand8(uint32_t n, const uint32_t (&t)[4], uint32_t (&o)[4]) {
+  const uint32_t idx = FOUR ? n & 0x77777777u : n, up = idx >> 16;
+  const uint32_t la = prmt(t[0], t[1], idx), lb = prmt(t[0], t[1], up);
+  uint32_t ha = prmt(t[2], t[3], idx), hb = prmt(t[2], t[3], up);
+  if (FOUR) {
+    const uint32_t n4 = n << 4;
+    ha ^= prmt(n, n4, 0x1504) & 0x80808080u;
+    hb ^= prmt(n, n4, 0x3726) & 0x80808080u;
+  }
+  o[0] = prmt(la, ha, 0x5140);
+  o[1] = prmt(la, ha, 0x7362);
+  o[2] = prmt(lb, hb, 0x5140);
+  o[3] = prmt(lb, hb, 0x7362);
+}
+
+// fp16 bytes of 8 table entries for byte permutes: the entries themselves (up
+// to 3 bits), or the magnitudes of a 4-bit odd-symmetric codebook.
+inline void byte_table(const float *c, int bits, uint32_t (&t)[4]) {
+  t[0] = t[1] = t[2] = t[3] = 0u;
+  for (int i = 0; i < 8; ++i) {
+    const float v = bits == 4 ? c[8 + i] : (i < (1 << bits) ? c[i] : 0.f);
+    const __half h = __float2half_rn(v);
+    uint16_t u;
+    memcpy(&u, &h, 2);
+    t[i / 4] |= static_cast<uint32_t>(u & 0xff) << (8 * (i % 4));
+    t[2 + i / 4] |= static_cast<uint32_t>(u >> 8) << (8 * (i % 4));
+  }
+}
