@@ -114,60 +114,6 @@ __device__ __forceinline__ int code_f64(double u, const float *t) {
   return n;
 }
 
-// Whole key row by one warp; whether the row was bad (coded as the zero row).
-// buf: d doubles of this warp.
-template <int D>
-__device__ __noinline__ bool key_row_f64(const PagedQuantArgs &a, int64_t off, int64_t pos, int64_t row, double *buf,
-                                         int lane) {
-  constexpr int NPL = D / 32;
-  const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
-  double x[NPL];
-  bool bad;
-  load_f64<NPL>(x, a.k, off, a.dtype, a.rc, a.rs, pos, lane);
-  const double nu = unit_f64<NPL>(x, a.books, buf, lane, bad);
-  uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + row * planes * (D / 8));
-  double r2 = 0.0;
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    const int idx = code_f64(x[k], a.books.tk);
-    for (int p = 0; p < mbk; ++p) {
-      const uint32_t w = __ballot_sync(TQ_FULL, (idx >> p) & 1);
-      if (lane == 0) krow[p * NPL + k] = w;
-    }
-    const double r = x[k] - static_cast<double>(a.books.ck[idx]);
-    buf[lane + 32 * k] = r;
-    r2 += r * r;
-  }
-  double rho = 0.0;
-  if (a.books.qjl) {
-    rho = sqrt(warp_sum_f64(r2));
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      const uint4 *sr = reinterpret_cast<const uint4 *>(a.S + (lane + 32 * k) * D);
-      double z = 0.0;
-#pragma unroll 4
-      for (int j = 0; j < D / 8; ++j) {
-        const uint4 v = sr[j];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z = fma(static_cast<double>(__uint_as_float(w[e] << 16)), buf[8 * j + 2 * e], z);
-          z = fma(static_cast<double>(__uint_as_float(w[e] & 0xffff0000u)), buf[8 * j + 2 * e + 1], z);
-        }
-      }
-      const uint32_t w = __ballot_sync(TQ_FULL, z >= 0.0);
-      if (lane == 0) krow[mbk * NPL + k] = w;
-    }
-    __syncwarp();
-  }
-  if (lane == 0)
-    reinterpret_cast<uint32_t *>(a.kscale)[row] =
-        __half_as_ushort(__double2half(nu)) | (static_cast<uint32_t>(__half_as_ushort(__double2half(rho))) << 16);
-  return bad;
-}
-
 // Bits of one token in its group's column words.
 template <int D>
 __device__ __forceinline__ void store_value_bits(const PagedQuantArgs &a, int64_t row, const int (&idx)[D / 32],

@@ -23,9 +23,12 @@
 namespace {
 
 constexpr int TR = 128;             // cache rows of a tile
+// Bytes between the 16-byte slices of a row operand: 16 more than its 128 rows
+// take, so that lanes that hold consecutive slices of one row write different banks.
+constexpr uint32_t XS = TR * 16 + 16;
 constexpr int GT = 256;             // threads of a group (one tile); two groups a block
 constexpr int LIST = 512;           // rows to code again, per group
-constexpr float BAND = 2.5e-6f;     // of |u - t|
+constexpr float BAND = 1.25e-6f;    // of |u - t|
 constexpr float ZBAND = 2.5e-6f;    // of |z| / (max |S| |r|)
 
 struct FixRow {
@@ -76,29 +79,47 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Eight consecutive input elements.
+// Eight consecutive input elements, as loaded.
 template <bool BF16>
-__device__ __forceinline__ void load8(float (&v)[8], const void *base, int64_t off) {
-  if (BF16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+  uint4 u[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void *base, int64_t off) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + off * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  } else {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) u[i] = __ldg(p + i);
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    if (BF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    } else {
+      const uint4 b = u[BF16 ? 0 : 1];
+      const uint32_t z[8] = {w[0], w[1], w[2], w[3], b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(z[e]);
+    }
+  }
+};
 
 __device__ __forceinline__ void load8f(float (&v)[8], const float *p) {
   const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// 1 where a >= t, else 0 (one compare, no predicate).
+__device__ __forceinline__ float at_least(float a, float t) {
+  float r;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(t));
+  return r;
 }
 
 // Code words from the sign words of |y| - t_k (d[0..HK-2], ascending t_k > 0)
@@ -121,20 +142,23 @@ __device__ __forceinline__ void planes(const uint32_t (&d)[1 << (NB - 1)], uint3
 
 // One tile of a group: sequence, first position, and what lies where.
 struct Tile {
+  int64_t unit = -1;
   int s, pos0, tile0, h;   // pos0: position of new token 0; tile0: first position of the tile
   SeqSpan sp;
   bool on;
 };
 
-__device__ __forceinline__ Tile find_tile(const PagedQuantArgs &a, int64_t unit) {
-  Tile t;
+// A group's items are consecutive heads of few units: the unit is looked up when
+// it changes.
+__device__ __forceinline__ void find_tile(const PagedQuantArgs &a, int64_t unit, Tile &t) {
+  if (unit == t.unit) return;
+  t.unit = unit;
   t.s = paged_find_seq(a.p, static_cast<int>(unit), TR, 2);
   t.sp = paged_span(a.p, t.s);
   t.pos0 = t.sp.len - t.sp.n;
   const int lt = static_cast<int>(unit) - paged_unit_base(a.p, t.s, TR, 2);
   t.tile0 = ((max(t.pos0, 0) >> 7) + lt) << 7;
   t.on = lt >= 0 && t.sp.n > 0 && t.tile0 < t.sp.len;
-  return t;
 }
 
 // What a scaled row carries on.  e: power of two taken out, nu 2^-e in [2^9, 2^10).
@@ -143,12 +167,18 @@ struct RowScale {
   bool bad, again;
 };
 
+// sqrt.approx is within 2^-23: nu may round to the neighbouring fp16 value, and
+// thresholds move by less than BAND.
 __device__ __forceinline__ RowScale row_scale(float ss, float amax) {
   RowScale r;
   r.bad = !(ss <= 4.3e9f);                      // not finite, or a norm beyond fp16 for sure
   r.again = !r.bad && (ss > 4.2e9f || (ss < 1e-24f && amax > 0.f));
-  r.nu = r.bad ? 0.f : sqrtf(ss);
-  r.f = r.nu > 0.f ? ldexpf(1.f, 9 - ilogbf(r.nu)) : 0.f;
+  float nu;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(nu) : "f"(ss));
+  r.nu = r.bad ? 0.f : nu;
+  // 2^(9 - exponent of nu); a norm below 2^-100 is coded again anyway
+  const int e = max(static_cast<int>(__float_as_uint(nu) >> 23), 27);
+  r.f = r.nu > 0.f ? __uint_as_float(static_cast<uint32_t>(263 - e) << 23) : 0.f;
   return r;
 }
 
@@ -156,40 +186,116 @@ __device__ __forceinline__ RowScale row_scale(float ss, float amax) {
 template <int D, int R>
 __device__ __forceinline__ void fill_rotation(uint8_t *dst, const TqBooks &bk, int tid, int nt) {
   for (int e = tid; e < R * (R / 8); e += nt) {
-    const int i = e % R, c = e / R;          // row, 16-byte slice of eight inputs
+    const int i = e % R, c = e / R;          // row, 16-byte slice of inputs 8 c .. 8 c + 7
+    const int id = i % D, j0 = (8 * c) % D;
+    uint32_t neg = bk.dneg[j0 >> 5] >> (j0 & 31);    // bit q: input j0 + q is negated
+    if (__popc(id & j0) & 1) neg = ~neg;
+    if (id & 1) neg ^= 0xaau;                        // parity of (id & 7) & q, bit by bit
+    if (id & 2) neg ^= 0xccu;
+    if (id & 4) neg ^= 0xf0u;
+    const bool on = i / D == 8 * c / D;
     uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t hw[2];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int j = 8 * c + 2 * q + z;
-        const bool neg = (__popc((i % D) & (j % D)) + (bk.dneg[(j % D) >> 5] >> (j & 31))) & 1;
-        hw[z] = i / D != j / D ? 0u : neg ? 0xbc00u : 0x3c00u;
-      }
-      w[q] = hw[0] | (hw[1] << 16);
-    }
+    for (int q = 0; q < 4; ++q)
+      w[q] = on ? 0x3c003c00u ^ ((neg >> (2 * q) & 1u) << 15) ^ ((neg >> (2 * q + 1) & 1u) << 31) : 0u;
     *reinterpret_cast<uint4 *>(dst + c * (R * 16) + (i >> 3) * 128 + (i & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// A key row coded again: u, codes and residual in 64 bits; its sketch values in fp32
+// from the operand copy of S, and in 64 bits where they come near zero.
+template <int D, bool QJL>
+__device__ __noinline__ bool fix_key(const PagedQuantArgs &a, const FixRow &f, const uint8_t *ss, float smax,
+                                     double *buf, int lane) {
+  constexpr int NPL = D / 32;
+  const int mbk = a.books.mse_bits_k, planes = mbk + QJL;
+  float *rf = reinterpret_cast<float *>(buf + D);
+  double x[NPL];
+  bool bad;
+  load_f64<NPL>(x, a.k, f.tok * a.st + f.h * a.sh, a.dtype, a.rc, a.rs, f.pos, lane);
+  const double nu = unit_f64<NPL>(x, a.books, buf, lane, bad);
+  uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + f.row * planes * (D / 8));
+  double r2 = 0.0;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) {
+    const int idx = code_f64(x[k], a.books.tk);
+    for (int p = 0; p < mbk; ++p) {
+      const uint32_t w = __ballot_sync(TQ_FULL, (idx >> p) & 1);
+      if (lane == 0) krow[p * NPL + k] = w;
+    }
+    const double r = x[k] - static_cast<double>(a.books.ck[idx]);
+    buf[lane + 32 * k] = r;
+    rf[lane + 32 * k] = static_cast<float>(r);
+    r2 += r * r;
+  }
+  double rho = 0.0;
+  if (QJL) {
+    rho = sqrt(warp_sum_f64(r2));
+    __syncwarp();
+    float z[NPL][4];
+#pragma unroll
+    for (int k = 0; k < NPL; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[k][e] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const float4 r0 = *reinterpret_cast<const float4 *>(rf + 8 * c), r1 = *reinterpret_cast<const float4 *>(rf + 8 * c + 4);
+      const float rv[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        const int i = lane + 32 * k;
+        const uint4 u = *reinterpret_cast<const uint4 *>(ss + c * (D * 16) + (i >> 3) * 128 + (i & 7) * 16);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+          z[k][e] = fmaf(v.x, rv[2 * e], fmaf(v.y, rv[2 * e + 1], z[k][e]));
+        }
+      }
+    }
+    // sums of d / 4 products and two more steps: 2^-23 (d / 4 + 2) |S_i| |r| at most
+    const float near = 4e-9f * (D + 8) * sqrtf(static_cast<float>(D)) * smax * static_cast<float>(rho);
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) {
+      const float zk = (z[k][0] + z[k][1]) + (z[k][2] + z[k][3]);
+      uint32_t sg = __ballot_sync(TQ_FULL, zk >= 0.f), again = __ballot_sync(TQ_FULL, !(fabsf(zk) > near));
+      while (again) {
+        const int b = __ffs(again) - 1, i = 32 * k + b;
+        again &= again - 1;
+        double part = 0.0;
+#pragma unroll
+        for (int q = 0; q < NPL; ++q)
+          part = fma(static_cast<double>(tq_bf16_to_f32(a.S[i * D + lane + 32 * q])), buf[lane + 32 * q], part);
+        sg = warp_sum_f64(part) >= 0.0 ? sg | (1u << b) : sg & ~(1u << b);
+      }
+      if (lane == 0) krow[mbk * NPL + k] = sg;
+    }
+    __syncwarp();
+  }
+  if (lane == 0)
+    reinterpret_cast<uint32_t *>(a.kscale)[f.row] =
+        __half_as_ushort(__double2half(nu)) | (static_cast<uint32_t>(__half_as_ushort(__double2half(rho))) << 16);
+  return bad;
 }
 
 // ------------------------------------------------------------------ keys
 
 template <int D>
-constexpr size_t key_smem() { return 2 * D * D * 2 + 2 * 2 * TR * D * 2; }
+constexpr size_t key_smem() { return 2 * D * D * 2 + 2 * 2 * (D / 8) * XS; }
 
 template <int D, int NB, bool QJL, bool BF16>
 __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_constant__ PagedQuantArgs a) {
   constexpr int HK = 1 << (NB - 1), LPR = D / 16, RPI = 32 / LPR, PL = NB + (QJL ? 1 : 0), NPL = D / 32;
-  constexpr uint32_t XB = TR * D * 2;                    // one operand term
+  constexpr uint32_t XB = (D / 8) * XS;                  // one operand term
   constexpr uint32_t ID = sm100::idesc_f16(TR, D);
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t bars[2];
   __shared__ uint32_t tmem_s;
   __shared__ int smax_s, nfix[2], abort_s;
-  __shared__ float rsc[2][TR], rnu[2][TR], r2s[2][2][TR];
-  __shared__ int rst[2][TR];           // 1: row of the call, 2: code again, 4: zero row
-  __shared__ int64_t rrow[2][TR];      // cache row
+  __shared__ float2 rsq[2][TR];        // a row's sum of squares and largest element
+  __shared__ float r2s[2][2][TR];
+  __shared__ uint32_t listed[2][TR / 32];
   __shared__ FixRow fix[2][LIST];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = tid / GT, gt = tid % GT, wg = warp & 7;
   uint8_t *hs = sm, *ss = sm + D * D * 2, *xs = ss + D * D * 2 + g * 2 * XB;
@@ -234,101 +340,116 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
   bool ok = true;
   int committed = 0;
   auto drain = [&]() {
-    double *buf = reinterpret_cast<double *>(xs) + wg * D;
+    double *buf = reinterpret_cast<double *>(xs) + wg * 2 * D;
     for (int e = wg; e < nfix[g]; e += 8) {
       const FixRow f = fix[g][e];
-      if (key_row_f64<D>(a, f.tok * a.st + f.h * a.sh, f.pos, f.row, buf, lane) && lane == 0 && a.status)
+      if (fix_key<D, QJL>(a, f, ss, __int_as_float(smax_s), buf, lane) && lane == 0 && a.status)
         atomicAdd(a.status, 1u);
     }
   };
-  const int64_t total = a.units * a.Hkv;
-  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
-    Tile t = find_tile(a, w / a.Hkv);
+  const int64_t total = a.units * a.Hkv, gid = blockIdx.x * 2 + g, ng = 2 * gridDim.x;
+  const int64_t w1 = total * (gid + 1) / ng;
+  // ---- rows: LPR lanes a row, eight coordinates of each half a lane.  The rows of
+  // the next tile are loaded while this one is coded (bf16; fp32 rows take too many
+  // registers for that and are loaded when they are used).
+  constexpr int IT = 16 / RPI;
+  const int j = lane % LPR, rl = 16 * wg + lane / LPR;
+  Raw8<BF16> raw[IT][2];
+  Tile t;
+  auto fetch = [&](int64_t w) {
+    find_tile(a, w / a.Hkv, t);
     t.h = static_cast<int>(w % a.Hkv);
-    if (!t.on) continue;
-    // ---- rows: LPR lanes a row, eight coordinates of each half a lane
-    const int j = lane % LPR;
-    float c0[16 / RPI][8], c1[16 / RPI][8];
-    int pos[16 / RPI];
 #pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int r = 16 * wg + it * RPI + lane / LPR;
-      pos[it] = t.tile0 + r;
-      const int i = pos[it] - t.pos0;
-      const bool in = i >= 0 && i < t.sp.n;
-      if (in) {
+    for (int it = 0; it < IT; ++it) {
+      const int i = t.tile0 + rl + it * RPI - t.pos0;
+      if (t.on && i >= 0 && i < t.sp.n) {
         const int64_t off = static_cast<int64_t>(t.sp.row0 + i) * a.st + t.h * a.sh + 8 * j;
-        load8<BF16>(c0[it], a.k, off);
-        load8<BF16>(c1[it], a.k, off + D / 2);
+        raw[it][0].load(a.k, off);
+        raw[it][1].load(a.k, off + D / 2);
       } else {
-        pos[it] = -1;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c0[it][e] = c1[it][e] = 0.f;
+        raw[it][0].zero();
+        raw[it][1].zero();
       }
     }
+  };
+  int64_t w = total * gid / ng;
+  if (BF16 && w < w1) fetch(w);
+  for (; w < w1; ++w) {
+    if (!BF16) fetch(w);
+    if (!t.on) {
+      if (BF16 && w + 1 < w1) fetch(w + 1);
+      continue;
+    }
+    const int tile0 = t.tile0, pos0 = t.pos0, row0 = t.sp.row0, head = t.h;
+    // this thread's row of the coding step, and its page
+    const int r = (wg & 3) * 32 + lane, hf = wg >> 2, ir = tile0 + r - pos0;
+    const bool in = ir >= 0 && ir < t.sp.n, any = __any_sync(TQ_FULL, in);
+    const int page = any ? paged_page(a.p, t.s, tile0 + (r & ~31)) : -1;
+    const int64_t row = (static_cast<int64_t>(page) * a.Hkv + head) * P + ((tile0 + r) & (P - 1));
+    const bool store = in && page >= 0;
+    if (gt < TR / 32) listed[g][gt] = 0u;
 #pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int r = 16 * wg + it * RPI + lane / LPR;
-      if (a.rc != nullptr && pos[it] >= 0) {
-        float cs[8], sn[8];
-        load8f(cs, a.rc + static_cast<int64_t>(pos[it]) * (D / 2) + 8 * j);
-        load8f(sn, a.rs + static_cast<int64_t>(pos[it]) * (D / 2) + 8 * j);
+    for (int it2 = 0; it2 < IT; it2 += 2) {
+      float cs[2][8], sn[2][8];
+      if (a.rc != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = c0[it][e], v = c1[it][e];
-          c0[it][e] = u * cs[e] - v * sn[e];
-          c1[it][e] = v * cs[e] + u * sn[e];
+        for (int z = 0; z < 2; ++z) {
+          const int pos = tile0 + rl + (it2 + z) * RPI;
+          const int64_t at = static_cast<int64_t>(min(max(pos, 0), t.sp.len - 1)) * (D / 2) + 8 * j;
+          load8f(cs[z], a.rc + at);
+          load8f(sn[z], a.rs + at);
         }
       }
-      float s2 = 0.f, mx = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s2 = fmaf(c0[it][e], c0[it][e], fmaf(c1[it][e], c1[it][e], s2));
-        mx = fmaxf(mx, fmaxf(fabsf(c0[it][e]), fabsf(c1[it][e])));
-      }
+      for (int z = 0; z < 2; ++z) {
+        const int it = it2 + z, rr = rl + it * RPI;
+        float c0[8], c1[8];
+        raw[it][0].get(c0);
+        raw[it][1].get(c1);
+        if (a.rc != nullptr) {
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) {
-        s2 += __shfl_xor_sync(TQ_FULL, s2, o);
-        mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
-      }
-      const RowScale rs = row_scale(s2, mx);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c0[it][e] = rs.f > 0.f ? c0[it][e] * rs.f : 0.f;
-        c1[it][e] = rs.f > 0.f ? c1[it][e] * rs.f : 0.f;
-      }
-      uint4 hi, lo;
-      uint8_t *dst = xs + (r >> 3) * 128 + (r & 7) * 16;
-      split8(c0[it], hi, lo);
-      *reinterpret_cast<uint4 *>(dst + j * (TR * 16)) = hi;
-      *reinterpret_cast<uint4 *>(dst + XB + j * (TR * 16)) = lo;
-      split8(c1[it], hi, lo);
-      *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * (TR * 16)) = hi;
-      *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * (TR * 16)) = lo;
-      if (j == 0) {
-        int state = 0;
-        if (pos[it] >= 0) {
-          const int page = paged_page(a.p, t.s, pos[it]);
-          if (page >= 0) {
-            state = 1 | (rs.again ? 2 : 0) | (rs.nu > 0.f ? 0 : 4);
-            rrow[g][r] = (static_cast<int64_t>(page) * a.Hkv + t.h) * P + (pos[it] & (P - 1));
-            if (rs.bad && a.status) atomicAdd(a.status, 1u);
-          } else if (a.status) {
-            atomicAdd(a.status, 1u);
+          for (int e = 0; e < 8; ++e) {
+            const float u = c0[e], v = c1[e];
+            c0[e] = u * cs[z][e] - v * sn[z][e];
+            c1[e] = v * cs[z][e] + u * sn[z][e];
           }
         }
-        rst[g][r] = state;
-        rnu[g][r] = rs.nu;
-        rsc[g][r] = rs.nu > 0.f ? sqrtf(static_cast<float>(D)) * rs.nu * rs.f : 1.f;
+        float s2 = 0.f, mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s2 = fmaf(c0[e], c0[e], fmaf(c1[e], c1[e], s2));
+          mx = fmaxf(mx, fmaxf(fabsf(c0[e]), fabsf(c1[e])));
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) {
+          s2 += __shfl_xor_sync(TQ_FULL, s2, o);
+          mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+        }
+        const RowScale rs = row_scale(s2, mx);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c0[e] = rs.f > 0.f ? c0[e] * rs.f : 0.f;
+          c1[e] = rs.f > 0.f ? c1[e] * rs.f : 0.f;
+        }
+        uint4 hi, lo;
+        uint8_t *dst = xs + (rr >> 3) * 128 + (rr & 7) * 16;
+        split8(c0, hi, lo);
+        *reinterpret_cast<uint4 *>(dst + j * XS) = hi;
+        *reinterpret_cast<uint4 *>(dst + XB + j * XS) = lo;
+        split8(c1, hi, lo);
+        *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * XS) = hi;
+        *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * XS) = lo;
+        if (j == 0) rsq[g][rr] = make_float2(s2, mx);
       }
     }
+    if (BF16 && w + 1 < w1) fetch(w + 1);
     sm100::fence_async_smem();
     if (!(ok = group_ok(1 + g, ok))) break;
     if (gt == 0) {
 #pragma unroll
       for (int q = 0; q < 2 * D / 16; ++q) {
         const int term = q / (D / 16), k = q % (D / 16);
-        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * (TR * 16), TR * 16, 128),
+        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * XS, XS, 128),
                            sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (D * 16), D * 16, 128), ID, q > 0 ? 1u : 0u);
       }
       sm100::mma_commit(&bars[g]);
@@ -338,26 +459,26 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
     ph ^= 1;
     sm100::fence_after_sync();
     // ---- codes: a thread a row and half of its coordinates
-    const int r = (wg & 3) * 32 + lane, hf = wg >> 2;
     const uint32_t ty = sm100::tmem_lane(tg, wg & 3);
-    const int state = rst[g][r];
-    const float sc = rsc[g][r];
-    uint64_t th[HK];
-    float cen[HK];
+    const RowScale rs = row_scale(rsq[g][r].x, rsq[g][r].y);
+    const bool zero = !(rs.nu > 0.f);
+    const float sc = zero ? 1.f : sqrtf(static_cast<float>(D)) * rs.nu * rs.f;
+    // thresholds above zero, and the centroids as the first one and steps
+    float th[HK], step[HK];
 #pragma unroll
-    for (int k = 0; k < HK; ++k) {
-      if (k < HK - 1) th[k] = pk2(a.books.tk[HK + k] * sc, a.books.tk[HK + k] * sc);
-      cen[k] = a.books.ck[HK + k] * sc;
+    for (int k = 0; k < HK - 1; ++k) {
+      th[k] = a.books.tk[HK + k] * sc;
+      step[k] = (a.books.ck[HK + k + 1] - a.books.ck[HK + k]) * sc;
     }
+    const float cen0 = a.books.ck[HK] * sc;
     float dist = 1e30f, r2 = 0.f;
-    uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode) + (state & 1 ? rrow[g][r] : 0) * PL * NPL + hf * (NPL / 2);
-    const bool store = state & 1;
+    uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode) + (store ? row : 0) * PL * NPL + hf * (NPL / 2);
 #pragma unroll
     for (int ch = 0; ch < NPL / 2; ++ch) {
       uint32_t yv[32];
       sm100::tmem_ld32(ty + hf * (D / 2) + 32 * ch, yv);
       sm100::wait_ld();
-      if (state & 4) {
+      if (zero) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) yv[e] = 0u;      // u = +0 decides the upper half
       }
@@ -368,24 +489,23 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
       for (int e = 30; e >= 0; e -= 2) {
         const float y0 = __uint_as_float(yv[e]), y1 = __uint_as_float(yv[e + 1]);
         const float a0 = fabsf(y0), a1 = fabsf(y1);
-        float m0 = cen[0], m1 = cen[0];
+        float r0 = a0 - cen0, r1 = a1 - cen0;
         dist = fminf(dist, fminf(a0, a1));
 #pragma unroll
         for (int k = 0; k < HK - 1; ++k) {
           float d0, d1;
-          sub2(a0, a1, th[k], d0, d1);
+          sub2(a0, a1, pk2(th[k], th[k]), d0, d1);
           dw[k] = __funnelshift_l(__float_as_uint(d1), dw[k], 1);
           dw[k] = __funnelshift_l(__float_as_uint(d0), dw[k], 1);
           dist = fminf(dist, fminf(fabsf(d0), fabsf(d1)));
           if (QJL) {
-            m0 = d0 >= 0.f ? cen[k + 1] : m0;
-            m1 = d1 >= 0.f ? cen[k + 1] : m1;
+            r0 = fmaf(at_least(d0, 0.f), -step[k], r0);
+            r1 = fmaf(at_least(d1, 0.f), -step[k], r1);
           }
         }
         dw[HK - 1] = __funnelshift_l(yv[e + 1], dw[HK - 1], 1);
         dw[HK - 1] = __funnelshift_l(yv[e], dw[HK - 1], 1);
         if (QJL) {
-          const float r0 = a0 - m0, r1 = a1 - m1;
           r2 = fmaf(r0, r0, fmaf(r1, r1, r2));
           yv[e] = __float_as_uint(r0) ^ (yv[e] & 0x80000000u);
           yv[e + 1] = __float_as_uint(r1) ^ (yv[e + 1] & 0x80000000u);
@@ -416,7 +536,7 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
         }
       }
     }
-    bool near = (state & 2) || (!(state & 4) && !(dist > BAND * sc));
+    bool near = rs.again || (!zero && !(dist > BAND * sc));
     float rho = 0.f;
     if (QJL) {
       sm100::wait_st();
@@ -451,15 +571,17 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
       }
       near |= !(zmin > zband * rho);
     }
-    if (store && hf == 0)
-      reinterpret_cast<uint32_t *>(a.kscale)[rrow[g][r]] =
-          tq_f32_to_half(rnu[g][r]) | (static_cast<uint32_t>(tq_f32_to_half(rho / sc)) << 16);
-    if (store && near && !(atomicOr(&rst[g][r], 8) & 8)) {
+    if (store && hf == 0) {
+      reinterpret_cast<uint32_t *>(a.kscale)[row] =
+          tq_f32_to_half(rs.nu) | (static_cast<uint32_t>(tq_f32_to_half(rho / sc)) << 16);
+    }
+    if (in && hf == 0 && (rs.bad || page < 0) && a.status) atomicAdd(a.status, 1u);
+    if (store && near && !((atomicOr(&listed[g][r >> 5], 1u << lane) >> lane) & 1u)) {
       FixRow f;
-      f.row = rrow[g][r];
-      f.pos = t.tile0 + r;
-      f.tok = t.sp.row0 + f.pos - t.pos0;
-      f.h = t.h;
+      f.row = row;
+      f.pos = tile0 + r;
+      f.tok = row0 + f.pos - pos0;
+      f.h = head;
       fix[g][atomicAdd(&nfix[g], 1)] = f;
     }
     if (!(ok = group_ok(1 + g, ok))) break;
@@ -488,14 +610,14 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
 // ------------------------------------------------------------------ values
 
 template <bool BF16>
-constexpr size_t value_smem() { return 128 * 128 * 2 + 2 * (BF16 ? 1 : 2) * TR * 128 * 2; }
+constexpr size_t value_smem() { return 128 * 128 * 2 + 2 * (BF16 ? 1 : 2) * 16 * XS; }
 
 // A tile's product has 128 lanes: the coordinates of one head (d = 128) or of two
 // (d = 64).
 template <int D, int NB, bool BF16>
 __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_constant__ PagedQuantArgs a) {
   constexpr int HK = 1 << (NB - 1), NH = 128 / D, LPR = D / 16, RPI = 32 / LPR, TERMS = BF16 ? 1 : 2;
-  constexpr uint32_t XB = TR * 128 * 2;
+  constexpr uint32_t XB = 16 * XS;
   constexpr uint32_t ID = sm100::idesc_f16(128, TR);
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t bars[2];
@@ -535,11 +657,40 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
     }
   };
   const int hgroups = (a.Hkv + NH - 1) / NH;
-  const int64_t total = a.units * hgroups;
-  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
-    Tile t = find_tile(a, w / hgroups);
+  const int64_t total = a.units * hgroups, gid = blockIdx.x * 2 + g, ng = 2 * gridDim.x;
+  const int64_t w1 = total * (gid + 1) / ng;
+  constexpr int IT = 16 / RPI;
+  const int j = lane % LPR, rl = 16 * wg + lane / LPR;
+  Raw8<BF16> raw[NH][IT][2];
+  Tile t;
+  // rows of an item; those of the next are loaded while this one is coded
+  auto fetch = [&](int64_t w) {
+    find_tile(a, w / hgroups, t);
     t.h = static_cast<int>(w % hgroups) * NH;
-    if (!t.on) continue;
+#pragma unroll
+    for (int hh = 0; hh < NH; ++hh)
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int i = t.tile0 + rl + it * RPI - t.pos0;
+        if (t.on && t.h + hh < a.Hkv && i >= 0 && i < t.sp.n) {
+          const int64_t off = static_cast<int64_t>(t.sp.row0 + i) * a.st + (t.h + hh) * a.sh + 8 * j;
+          raw[hh][it][0].load(a.v, off);
+          raw[hh][it][1].load(a.v, off + D / 2);
+        } else {
+          raw[hh][it][0].zero();
+          raw[hh][it][1].zero();
+        }
+      }
+  };
+  int64_t w = total * gid / ng;
+  if (BF16 && w < w1) fetch(w);
+  for (; w < w1; ++w) {
+    if (!BF16) fetch(w);
+    if (!t.on) {
+      if (BF16 && w + 1 < w1) fetch(w + 1);
+      continue;
+    }
+    const int tile0 = t.tile0, pos0 = t.pos0, row0 = t.sp.row0, head = t.h;
     if (gt < TR) {
       // which rows the call brings, a warp a 32-token group
       const int pos = t.tile0 + gt, i = pos - t.pos0, p32 = t.tile0 + (gt & ~31);
@@ -556,31 +707,20 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
       }
     }
     if (!(ok = group_ok(1 + g, ok))) break;
-    const int j = lane % LPR;
 #pragma unroll
     for (int hh = 0; hh < NH; ++hh) {
-      const bool head = t.h + hh < a.Hkv;
-      float c0[16 / RPI][8], c1[16 / RPI][8];
 #pragma unroll
-      for (int it = 0; it < 16 / RPI; ++it) {
-        const int r = 16 * wg + it * RPI + lane / LPR, i = t.tile0 + r - t.pos0;
-        if (head && ((act[g][r >> 5] >> (r & 31)) & 1u)) {
-          const int64_t off = static_cast<int64_t>(t.sp.row0 + i) * a.st + (t.h + hh) * a.sh + 8 * j;
-          load8<BF16>(c0[it], a.v, off);
-          load8<BF16>(c1[it], a.v, off + D / 2);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) c0[it][e] = c1[it][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < 16 / RPI; ++it) {
-        const int r = 16 * wg + it * RPI + lane / LPR;
+      for (int it = 0; it < IT; ++it) {
+        const int r = rl + it * RPI;
+        const bool in = head + hh < a.Hkv && ((act[g][r >> 5] >> (r & 31)) & 1u);
+        float c0[8], c1[8];
+        raw[hh][it][0].get(c0);
+        raw[hh][it][1].get(c1);
         float s2 = 0.f, mx = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s2 = fmaf(c0[it][e], c0[it][e], fmaf(c1[it][e], c1[it][e], s2));
-          mx = fmaxf(mx, fmaxf(fabsf(c0[it][e]), fabsf(c1[it][e])));
+          s2 = fmaf(c0[e], c0[e], fmaf(c1[e], c1[e], s2));
+          mx = fmaxf(mx, fmaxf(fabsf(c0[e]), fabsf(c1[e])));
         }
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) {
@@ -590,20 +730,20 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
         const RowScale rs = row_scale(s2, mx);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          c0[it][e] = rs.f > 0.f ? c0[it][e] * rs.f : 0.f;
-          c1[it][e] = rs.f > 0.f ? c1[it][e] * rs.f : 0.f;
+          c0[e] = rs.f > 0.f ? c0[e] * rs.f : 0.f;
+          c1[e] = rs.f > 0.f ? c1[e] * rs.f : 0.f;
         }
         uint4 hi, lo;
-        uint8_t *dst = xs + hh * (D / 8) * (TR * 16) + (r >> 3) * 128 + (r & 7) * 16;
-        split8(c0[it], hi, lo);
-        *reinterpret_cast<uint4 *>(dst + j * (TR * 16)) = hi;
-        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + j * (TR * 16)) = lo;
-        split8(c1[it], hi, lo);
-        *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * (TR * 16)) = hi;
-        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * (TR * 16)) = lo;
+        uint8_t *dst = xs + hh * (D / 8) * XS + (r >> 3) * 128 + (r & 7) * 16;
+        split8(c0, hi, lo);
+        *reinterpret_cast<uint4 *>(dst + j * XS) = hi;
+        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + j * XS) = lo;
+        split8(c1, hi, lo);
+        *reinterpret_cast<uint4 *>(dst + (D / 16 + j) * XS) = hi;
+        if (!BF16) *reinterpret_cast<uint4 *>(dst + XB + (D / 16 + j) * XS) = lo;
         if (j == 0) {
-          rinv[g][hh][r] = rs.nu > 0.f ? 1.0f / (sqrtf(static_cast<float>(D)) * rs.nu * rs.f) : 0.f;
-          if (head && ((act[g][r >> 5] >> (r & 31)) & 1u)) {
+          rinv[g][hh][r] = rs.nu > 0.f ? __frcp_rn(sqrtf(static_cast<float>(D)) * rs.nu * rs.f) : 0.f;
+          if (in) {
             a.vnorm[grow[g][r >> 5] + static_cast<int64_t>(hh) * P + (r & 31)] = tq_f32_to_half(rs.nu);
             if (rs.bad && a.status) atomicAdd(a.status, 1u);
             if (rs.again) atomicOr(&near[g][hh][r >> 5], 1u << (r & 31));
@@ -612,6 +752,7 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
         }
       }
     }
+    if (BF16 && w + 1 < w1) fetch(w + 1);
     sm100::fence_async_smem();
     if (!(ok = group_ok(1 + g, ok))) break;
     if (gt == 0) {
@@ -619,7 +760,7 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
       for (int q = 0; q < TERMS * 8; ++q) {
         const int term = q / 8, k = q % 8;
         sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (128 * 16), 128 * 16, 128),
-                           sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * (TR * 16), TR * 16, 128), ID,
+                           sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * XS, XS, 128), ID,
                            q > 0 ? 1u : 0u);
       }
       sm100::mma_commit(&bars[g]);
@@ -640,7 +781,7 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
       sm100::tmem_ld32(sm100::tmem_lane(tg, lq) + 32 * gr, yv);
       sm100::wait_ld();
       const uint32_t on = act[g][gr];
-      if (on == 0u || t.h + hh >= a.Hkv) continue;
+      if (on == 0u || head + hh >= a.Hkv) continue;
       uint32_t dw[HK];
       float dist = 1e30f;
 #pragma unroll
@@ -697,9 +838,9 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
       if (((near[g][nh][r >> 5] & act[g][r >> 5]) >> (r & 31)) & 1u) {
         FixRow f;
         f.row = grow[g][r >> 5] + static_cast<int64_t>(nh) * P + (r & 31);
-        f.pos = t.tile0 + r;
-        f.tok = t.sp.row0 + f.pos - t.pos0;
-        f.h = t.h + nh;
+        f.pos = tile0 + r;
+        f.tok = row0 + f.pos - pos0;
+        f.h = head + nh;
         const int at = atomicAdd(&nfix[g], 1);
         if (at < LIST) fix[g][at] = f;
       }
