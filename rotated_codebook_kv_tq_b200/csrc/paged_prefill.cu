@@ -3,7 +3,7 @@
 // 1. The pages are expanded once into operand tiles of 128 tokens, in the
 //    rotated domain and in the layout that the tensor cores read:
 //      K^_j = 2^-E nu_j (c[idx_j] + coef rho_j S^T (2 sigma_j - 1))   fp16
-//      V^_j = 2^-F nu^v_j c_v[idx^v_j]                                 fp16, transposed
+//      V^_j = 2^-F nu^v_j c_v[idx^v_j]                         fp16 (table and product), transposed
 //    with 2^E, 2^F just above the tile's largest norms, so entries are at most
 //    1 and a token far below the tile's largest loses only absolute precision
 //    (2^-25 of that largest).  The sketch's part of a logit,
@@ -20,7 +20,7 @@
 
 #include <cstdlib>
 
-#include "paged.h"
+#include "paged_expand.cuh"
 #include "tq_sm100.cuh"
 
 namespace {
@@ -63,6 +63,7 @@ struct PrefillArgs {
   float *po;                 // [N Hq][splits][D]
   float2 *pml;
   uint32_t wait_outer;
+  uint32_t lutk[4], lutv[4];
   TqBooks books;
 };
 
@@ -72,42 +73,45 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
-  return d;
-}
-
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // ------------------------------------------------------------------ expansion
+//
+// Orders.  Table lookups leave the eight elements 4 e + s (e = 0 .. 7) of a plane
+// word together, so a tile keeps them together: token 4 e + s of a 32-token group is
+// at place 8 s + e of the tile's key rows and value columns, and coordinate 4 e + s
+// of a word at place 8 s + e of a key row (d = 64: of a 16-coordinate half word,
+// 4 s + e).  Queries are laid out alike; sums do not see the order.
 
-// One block a token tile of a (sequence, KV head); EX tiles in a row share the
-// block's copy of S.
-constexpr int EX = 4;
+// Token of place n of a 32-token group.
+__host__ __device__ constexpr int place_token(int n) { return 4 * (n & 7) + (n >> 3); }
 
+// Place of coordinate c in a key or query row.
 template <int D>
-__global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant__ PrefillArgs a) {
+__device__ __forceinline__ int coord_place(int c) {
+  return D == 128 ? (c & ~31) + 8 * (c & 3) + ((c & 31) >> 2) : (c & ~15) + 4 * (c & 3) + ((c & 15) >> 2);
+}
+
+// Blocks walk the (token tile, KV head, sequence) items; each keeps the sketch
+// matrix as operand fragments in shared memory.
+template <int D, bool K4, bool V4>
+__global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int NPL = D / 32, KS = D / 16, NN = D / 8;
   extern __shared__ __align__(16) uint2 sfrag[];   // [KS][NN][32]
-  __shared__ float ckt[16], cvt[16], nuk[TK], nuv[TK], mx[8][2];
+  __shared__ float nuk[TK], mx[8][2];
+  __shared__ __align__(16) __half nuv[TK];         // by place
   __shared__ int page[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int s = blockIdx.z, hl = blockIdx.y, h = a.head0 + hl;
-  const SeqSpan sp = paged_span(a.p, s);
-  if (sp.n == 0 || static_cast<int64_t>(blockIdx.x) * EX * TK >= sp.len) return;
-  if (tid < 16) {
-    ckt[tid] = a.books.ck[tid];
-    cvt[tid] = a.books.cv[tid];
-  }
   if (a.books.qjl) {
-    // operand order: k-step ks, register r, half e of thread column t is
-    // coordinate 32 t + 2 ks + r + 16 e (d = 64: 16 t + 2 ks + r + 8 e) of the sketch
+    // k-step ks, register r, half e of thread column t: sketch row 32 t + 2 ks + r +
+    // 16 e (d = 64: 16 t + 2 ks + r + 8 e); column 2 t + b of n-tile nn: the coordinate
+    // that expand8 leaves in half b of pair nn of thread t's word
     for (int e = tid; e < KS * NN * 32; e += 256) {
-      const int l = e & 31, nn = (e >> 5) % NN, ks = (e >> 5) / NN, j = 8 * nn + (l >> 2);
+      const int l = e & 31, nn = (e >> 5) % NN, ks = (e >> 5) / NN, ct = l >> 3, b = (l >> 2) & 1;
+      const int j = D == 128 ? 32 * ct + 8 * (nn & 3) + 4 * b + (nn >> 2) : 16 * ct + 8 * (nn & 1) + 4 * b + (nn >> 1);
       uint32_t w[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -118,17 +122,22 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
     }
   }
   const int P = 1 << a.p.page_shift, mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
-  for (int tl = blockIdx.x * EX; tl < (blockIdx.x + 1) * EX && tl * TK < sp.len; ++tl) {
-    const int j0 = tl * TK;
+  const int64_t items = static_cast<int64_t>(a.max_tiles) * a.heads * a.p.num_seqs;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int tl = static_cast<int>(item % a.max_tiles), j0 = tl * TK;
+    const int hl = static_cast<int>(item / a.max_tiles % a.heads), h = a.head0 + hl;
+    const int s = static_cast<int>(item / a.max_tiles / a.heads);
+    const SeqSpan sp = paged_span(a.p, s);
+    if (sp.n == 0 || j0 >= sp.len) continue;
     uint8_t *img = a.tiles + ((static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles + tl) * tile_bytes(D);
     __syncthreads();   // the last tile's scales have been read
     if (tid < 4) page[tid] = j0 + 32 * tid < sp.len ? paged_page(a.p, s, j0 + 32 * tid) : -1;
     __syncthreads();
-    // row of token j of the tile
+    // cache row of token j of the tile
     auto row_of = [&](int j) {
       return (static_cast<int64_t>(page[j >> 5]) * a.Hkv + h) * P + ((j0 + j) & (P - 1));
     };
-    float nk = 0.f, rho = 0.f, nv = 0.f;
+    float nk = 0.f, nv = 0.f;
     const bool there = tid < TK && page[(tid & (TK - 1)) >> 5] >= 0 && j0 + tid < sp.len;
     if (there) {
       const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row_of(tid)];
@@ -152,7 +161,7 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
     const int ke = kmax > 0.f ? ilogbf(kmax) + 1 : 0, ve = vmax > 0.f ? ilogbf(vmax) + 1 : 0;
     if (tid < TK) {
       nuk[tid] = ldexpf(nk, -ke);
-      nuv[tid] = ldexpf(nv, -ve);
+      nuv[(tid & ~31) + 8 * (tid & 3) + ((tid & 31) >> 2)] = __float2half_rn(ldexpf(nv, -ve));
     }
     if (tid == 0) {
       TileHeader *hd = reinterpret_cast<TileHeader *>(img);
@@ -164,26 +173,40 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
       hd->all = all;
     }
     __syncthreads();
-    // ---- keys: warp w takes tokens 16 w .. 16 w + 15
+    // ---- keys: warp w takes places 16 w .. 16 w + 15, rows g and g + 8
     {
-      const int r0 = 16 * warp + g;
+      const int tk0 = 32 * (warp >> 1) + 4 * g + 2 * (warp & 1), tk1 = tk0 + 1;
       const bool on = page[warp >> 1] >= 0;
-      const int64_t base = on ? row_of(r0) : 0;
-      const uint32_t *kr0 = reinterpret_cast<const uint32_t *>(a.kcode + base * planes * (D / 8));
-      const uint32_t *kr1 = kr0 + 8 * planes * NPL;
-      const uint32_t *sc = reinterpret_cast<const uint32_t *>(a.kscale) + base;
+      const int64_t base = on ? row_of(tk0) : 0;
+      const uint32_t *kr0 = reinterpret_cast<const uint32_t *>(a.kcode + base * planes * (D / 8)) + (D == 128 ? t : t >> 1);
+      const uint32_t *kr1 = kr0 + planes * NPL;
+      uint32_t w0[4], w1[4], sg0 = 0u, sg1 = 0u, sc0 = 0u, sc1 = 0u;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        w0[p] = on && p < mbk ? kr0[p * NPL] : 0u;
+        w1[p] = on && p < mbk ? kr1[p * NPL] : 0u;
+      }
+      if (a.books.qjl && on) {
+        sg0 = kr0[mbk * NPL];
+        sg1 = kr1[mbk * NPL];
+        sc0 = reinterpret_cast<const uint32_t *>(a.kscale)[base];
+        sc1 = reinterpret_cast<const uint32_t *>(a.kscale)[base + 1];
+      }
+      if (D == 64) {
+        sg0 = prmt(sg0, 0u, t & 1 ? 0x4342 : 0x4140);
+        sg1 = prmt(sg1, 0u, t & 1 ? 0x4342 : 0x4140);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          w0[p] >>= 16 * (t & 1);
+          w1[p] >>= 16 * (t & 1);
+        }
+      }
       float acc[NN][4];
 #pragma unroll
       for (int n = 0; n < NN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-      float f0 = 0.f, f1 = 0.f;
       if (a.books.qjl && on) {
-        uint32_t sg0 = kr0[mbk * NPL + (D == 128 ? t : t >> 1)], sg1 = kr1[mbk * NPL + (D == 128 ? t : t >> 1)];
-        if (D == 64) {
-          sg0 = prmt(sg0, 0u, t & 1 ? 0x4342 : 0x4140);
-          sg1 = prmt(sg1, 0u, t & 1 ? 0x4342 : 0x4140);
-        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t a0 = ((sg0 << (15 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
@@ -199,40 +222,38 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
           }
         }
-        rho = tq_half_to_f32(static_cast<uint16_t>(sc[0] >> 16));
-        f0 = a.qjl_coef * rho;
-        f1 = a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc[8] >> 16));
       }
-      const float n0 = nuk[r0], n1 = nuk[r0 + 8];
       // rows past the end may hold anything: their factor is exactly zero
-      const bool e0 = n0 > 0.f, e1 = n1 > 0.f;
-      uint8_t *kimg = img + HDR;
+      const float n0 = nuk[tk0], n1 = nuk[tk1];
+      const float f0 = n0 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc0 >> 16)) : 0.f;
+      const float f1 = n1 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc1 >> 16)) : 0.f;
+      if (K4) {
+        fold_sign(w0);
+        fold_sign(w1);
+      }
+      // a thread's coordinates are places 32 t .. (d = 64: 16 t ..) of its rows
+      uint8_t *o = img + HDR + (D / 32) * t * (TK * 16) + 2 * warp * 128 + g * 16;
 #pragma unroll
-      for (int w = 0; w < NPL; ++w) {
-        uint32_t p0[4], p1[4];
+      for (int sft = 0; sft < 4; ++sft) {
+        uint32_t c0[4], c1[4];
+        expand8<K4>(nibbles<K4>(w0, sft), a.lutk, c0);
+        expand8<K4>(nibbles<K4>(w1, sft), a.lutk, c1);
+        constexpr int PR = D == 128 ? 4 : 2;      // pairs of a shift
+        uint32_t v0[PR], v1[PR];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          p0[p] = on && p < mbk ? kr0[p * NPL + w] : 0u;
-          p1[p] = on && p < mbk ? kr1[p * NPL + w] : 0u;
+        for (int i = 0; i < PR; ++i) {
+          const int n = PR * sft + i;
+          const float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&c0[i]));
+          const float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&c1[i]));
+          v0[i] = pack_half(n0 * fmaf(f0, acc[n][0], x0.x), n0 * fmaf(f0, acc[n][1], x0.y));
+          v1[i] = pack_half(n1 * fmaf(f1, acc[n][2], x1.x), n1 * fmaf(f1, acc[n][3], x1.y));
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = 4 * w + i, b = 8 * i + 2 * t;
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            int i0 = 0, i1 = 0;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              i0 |= ((p0[p] >> (b + e)) & 1u) << p;
-              i1 |= ((p1[p] >> (b + e)) & 1u) << p;
-            }
-            v[e] = e0 ? n0 * fmaf(f0, acc[n][e], ckt[i0]) : 0.f;
-            v[2 + e] = e1 ? n1 * fmaf(f1, acc[n][2 + e], ckt[i1]) : 0.f;
-          }
-          uint8_t *o = kimg + n * (TK * 16) + 2 * warp * 128 + g * 16 + t * 4;
-          *reinterpret_cast<uint32_t *>(o) = pack_half(v[0], v[1]);
-          *reinterpret_cast<uint32_t *>(o + 128) = pack_half(v[2], v[3]);
+        if (D == 128) {
+          *reinterpret_cast<uint4 *>(o + sft * (TK * 16)) = make_uint4(v0[0], v0[1], v0[PR - 2], v0[PR - 1]);
+          *reinterpret_cast<uint4 *>(o + sft * (TK * 16) + 128) = make_uint4(v1[0], v1[1], v1[PR - 2], v1[PR - 1]);
+        } else {
+          *reinterpret_cast<uint2 *>(o + (sft >> 1) * (TK * 16) + 8 * (sft & 1)) = make_uint2(v0[0], v0[1]);
+          *reinterpret_cast<uint2 *>(o + (sft >> 1) * (TK * 16) + 8 * (sft & 1) + 128) = make_uint2(v1[0], v1[1]);
         }
       }
     }
@@ -240,29 +261,24 @@ __global__ void __launch_bounds__(256) paged_expand_kernel(const __grid_constant
     for (int it = tid; it < 4 * D; it += 256) {
       const int c = it % D, gr = it / D;
       const bool on = page[gr] >= 0;
+      const uint32_t *vw = a.vcode + (on ? (row_of(32 * gr) >> 5) * nbv * D + c : 0);
       uint32_t w[4];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        w[p] = on && p < nbv ? a.vcode[((row_of(32 * gr) >> 5) * nbv + p) * D + c] : 0u;
-      uint8_t *vimg = img + HDR + TK * D * 2 + (c >> 3) * 128 + (c & 7) * 16;
+      for (int p = 0; p < 4; ++p) w[p] = on && p < nbv ? vw[p * D] : 0u;
+      if (V4) fold_sign(w);
+      uint8_t *vimg = img + HDR + TK * D * 2 + (c >> 3) * 128 + (c & 7) * 16 + 4 * gr * (D * 16);
 #pragma unroll
-      for (int k8 = 0; k8 < 4; ++k8) {
+      for (int sft = 0; sft < 4; ++sft) {
         uint32_t o[4];
+        expand8<V4>(nibbles<V4>(w, sft), a.lutv, o);
+        const uint4 nu = *reinterpret_cast<const uint4 *>(&nuv[32 * gr + 8 * sft]);
+        const uint32_t nw[4] = {nu.x, nu.y, nu.z, nu.w};
 #pragma unroll
-        for (int k2 = 0; k2 < 4; ++k2) {
-          float v[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int b = 8 * k8 + 2 * k2 + e;
-            int idx = 0;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) idx |= ((w[p] >> b) & 1u) << p;
-            const float nu = nuv[32 * gr + b];
-            v[e] = nu > 0.f ? nu * cvt[idx] : 0.f;
-          }
-          o[k2] = pack_half(v[0], v[1]);
+        for (int i = 0; i < 4; ++i) {
+          const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&o[i]), *reinterpret_cast<const __half2 *>(&nw[i]));
+          o[i] = *reinterpret_cast<const uint32_t *>(&r);
         }
-        *reinterpret_cast<uint4 *>(vimg + (4 * gr + k8) * (D * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(vimg + sft * (D * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -341,48 +357,59 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
   if (warp < 8) {
     const int x = warp >> 2;
     uint8_t *qimg = sm + L::Q + x * L::OPER;
-    for (int r = 32 * (warp & 3); r < 32 * (warp & 3) + 32; ++r) {
-      const int tt = r / a.G, tok = tok0 + x * a.tok_tile + tt, pos = pos0 + tok;
-      const bool on = tt < a.tok_tile && tok < sp.n && pos >= 0;
-      const int64_t off = static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + r % a.G) * a.sh;
-      float v[NPL];
+    constexpr int QB = 4;       // rows in flight
+#pragma unroll 1
+    for (int rb = 32 * (warp & 3); rb < 32 * (warp & 3) + 32; rb += QB) {
+      float v[QB][NPL], cs[QB][NPL / 2], sn[QB][NPL / 2];
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) v[k] = on ? tq_load_elem(a.q, off + lane + 32 * k, a.dtype) : 0.f;
-      if (a.rc != nullptr && on) {
+      for (int z = 0; z < QB; ++z) {
+        const int r = rb + z, tt = r / a.G, tok = tok0 + x * a.tok_tile + tt, pos = pos0 + tok;
+        const bool on = tt < a.tok_tile && tok < sp.n && pos >= 0;
+        const int64_t off = static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + r % a.G) * a.sh;
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) v[z][k] = on ? tq_load_elem(a.q, off + lane + 32 * k, a.dtype) : 0.f;
 #pragma unroll
         for (int k = 0; k < NPL / 2; ++k) {
-          const float c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-          const float sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-          const float p = v[k], w = v[k + NPL / 2];
-          v[k] = p * c - w * sn;
-          v[k + NPL / 2] = w * c + p * sn;
+          const bool rope = a.rc != nullptr && on;
+          cs[z][k] = rope ? a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k] : 1.f;
+          sn[z][k] = rope ? a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k] : 0.f;
         }
       }
-      float f = a.scale * 1.4426950408889634f;
-      if (a.books.pi != nullptr) {
-        // the value operands' place holds no tile yet
-        tq_warp_dense<NPL>(v, a.books.pi_t, reinterpret_cast<float *>(sm + L::V) + warp * D, lane);
-      } else {
-        tq_apply_signs<NPL>(v, a.books.dneg, lane);
-        tq_warp_wht<NPL>(v, lane);
-        f *= 1.0f / sqrtf(static_cast<float>(D));
-      }
-      float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) {
-        v[k] *= f;
-        m = fmaxf(m, fabsf(v[k]));
-      }
-      m = tq_warp_max(m);
-      // a power of two taken out where fp16 would lose digits or overflow
-      const int e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-120, min(120, ilogbf(m) + 1)) : 0;
+      for (int z = 0; z < QB; ++z) {
+        const int r = rb + z;
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) {
-        const int c = lane + 32 * k;
-        *reinterpret_cast<__half *>(qimg + (c >> 3) * (TQ * 16) + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2) =
-            __float2half_rn(e == 0 ? v[k] : ldexpf(v[k], -e));
+        for (int k = 0; k < NPL / 2; ++k) {
+          const float p = v[z][k], w = v[z][k + NPL / 2];
+          v[z][k] = p * cs[z][k] - w * sn[z][k];
+          v[z][k + NPL / 2] = w * cs[z][k] + p * sn[z][k];
+        }
+        float f = a.scale * 1.4426950408889634f;
+        if (a.books.pi != nullptr) {
+          // the value operands' place holds no tile yet
+          tq_warp_dense<NPL>(v[z], a.books.pi_t, reinterpret_cast<float *>(sm + L::V) + warp * D, lane);
+        } else {
+          tq_apply_signs<NPL>(v[z], a.books.dneg, lane);
+          tq_warp_wht<NPL, true>(v[z], lane);
+          f *= 1.0f / sqrtf(static_cast<float>(D));
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) {
+          v[z][k] *= f;
+          m = fmaxf(m, fabsf(v[z][k]));
+        }
+        m = tq_warp_max(m);
+        // a power of two taken out where fp16 would lose digits or overflow
+        const int e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-120, min(120, ilogbf(m) + 1)) : 0;
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) {
+          const int c = coord_place<D>(lane + 32 * k);
+          *reinterpret_cast<__half *>(qimg + (c >> 3) * (TQ * 16) + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2) =
+              __float2half_rn(e == 0 ? v[z][k] : ldexpf(v[z][k], -e));
+        }
+        if (lane == 0) frow[x][r] = ldexpf(1.f, e);
       }
-      if (lane == 0) frow[x][r] = ldexpf(1.f, e);
     }
     sm100::fence_async_smem();
   }
@@ -500,7 +527,7 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
           const uint32_t see = hd->there[c] & (lim < 0 ? 0u : lim >= 31 ? ~0u : (2u << lim) - 1u);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (!((see >> e) & 1u)) sv[c][e] = 0xff800000u;
+            if (!((see >> place_token(e)) & 1u)) sv[c][e] = 0xff800000u;
         }
       }
       float mx = -CUDART_INF_F;
@@ -674,7 +701,7 @@ Plan plan(const tq_codec *c, int N, int num_seqs, int max_len, int Hq, int Hkv) 
 }
 
 template <int D>
-int run_prefill(PrefillArgs &a, const Plan &pl, cudaStream_t stream) {
+int run_prefill(PrefillArgs &a, const Plan &pl, bool k4, bool v4, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   static bool done[64] = {};
@@ -688,8 +715,10 @@ int run_prefill(PrefillArgs &a, const Plan &pl, cudaStream_t stream) {
   for (int h0 = 0; h0 < a.Hkv; h0 += pl.heads) {
     a.head0 = h0;
     a.heads = std::min(pl.heads, a.Hkv - h0);
-    const dim3 eg((pl.max_tiles + EX - 1) / EX, a.heads, a.p.num_seqs);
-    paged_expand_kernel<D><<<eg, 256, es, stream>>>(a);
+    const int64_t items = static_cast<int64_t>(pl.max_tiles) * a.heads * a.p.num_seqs;
+    auto ex = k4 ? (v4 ? paged_expand_kernel<D, true, true> : paged_expand_kernel<D, true, false>)
+                 : (v4 ? paged_expand_kernel<D, false, true> : paged_expand_kernel<D, false, false>);
+    ex<<<static_cast<unsigned>(std::min<int64_t>(items, 2 * 148)), 256, es, stream>>>(a);
     if (int e = tq_check_launch("paged_expand_kernel")) return e;
     paged_prefill_kernel<D><<<dim3(pl.units, a.heads, pl.splits), 320, shm, stream>>>(a);
     if (int e = tq_check_launch("paged_prefill_kernel")) return e;
@@ -746,5 +775,8 @@ int launch_paged_prefill(const tq_codec *c, const PagedView &p, const void *q, i
   if (const char *e = getenv("TQ_WAIT_LIMIT"))
     a.wait_outer = static_cast<uint32_t>((strtoul(e, nullptr, 10) + (1u << 14) - 1) >> 14);
   a.books = c->books;
-  return c->d == 64 ? run_prefill<64>(a, pl, stream) : run_prefill<128>(a, pl, stream);
+  byte_table(c->books.ck, c->mse_bits_k, a.lutk);
+  byte_table(c->books.cv, c->bits_v, a.lutv);
+  const bool k4 = c->mse_bits_k == 4, v4 = c->bits_v == 4;
+  return c->d == 64 ? run_prefill<64>(a, pl, k4, v4, stream) : run_prefill<128>(a, pl, k4, v4, stream);
 }
