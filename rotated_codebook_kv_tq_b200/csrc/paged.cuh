@@ -69,3 +69,53 @@ __device__ __forceinline__ int paged_find_seq(const PagedView &p, int u, int per
   }
   return lo;
 }
+
+// R rows of a packed tensor, coordinate lane + 32 k of row z in x[z][k] (zeros where
+// off[z] < 0).  One branch on the type around all loads: a branch per element would
+// wait for each load before the next.
+template <int R, int NPL>
+__device__ __forceinline__ void paged_load_rows(float (&x)[R][NPL], const void *base, const int64_t (&off)[R], int dtype,
+                                                int lane) {
+  if (dtype == TQ_BF16) {
+    uint16_t h[R][NPL];
+#pragma unroll
+    for (int z = 0; z < R; ++z)
+#pragma unroll
+      for (int k = 0; k < NPL; ++k)
+        h[z][k] = off[z] >= 0 ? static_cast<const uint16_t *>(base)[off[z] + lane + 32 * k] : uint16_t{0};
+#pragma unroll
+    for (int z = 0; z < R; ++z)
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) x[z][k] = tq_bf16_to_f32(h[z][k]);
+  } else {
+#pragma unroll
+    for (int z = 0; z < R; ++z)
+#pragma unroll
+      for (int k = 0; k < NPL; ++k)
+        x[z][k] = off[z] >= 0 ? static_cast<const float *>(base)[off[z] + lane + 32 * k] : 0.f;
+  }
+}
+
+// Rotate-half position rotation of those rows at pos[z] (rows with off[z] < 0 stay).
+template <int R, int NPL>
+__device__ __forceinline__ void paged_rope_rows(float (&x)[R][NPL], const float *rc, const float *rs,
+                                                const int (&pos)[R], const int64_t (&off)[R], int lane) {
+  if (rc == nullptr) return;
+  float c[R][NPL / 2], s[R][NPL / 2];
+#pragma unroll
+  for (int z = 0; z < R; ++z)
+#pragma unroll
+    for (int k = 0; k < NPL / 2; ++k) {
+      const int64_t at = static_cast<int64_t>(off[z] >= 0 ? pos[z] : 0) * (NPL * 16) + lane + 32 * k;
+      c[z][k] = rc[at];
+      s[z][k] = rs[at];
+    }
+#pragma unroll
+  for (int z = 0; z < R; ++z)
+#pragma unroll
+    for (int k = 0; k < NPL / 2; ++k) {
+      const float u = x[z][k], v = x[z][k + NPL / 2];
+      x[z][k] = u * c[z][k] - v * s[z][k];
+      x[z][k + NPL / 2] = v * c[z][k] + u * s[z][k];
+    }
+}

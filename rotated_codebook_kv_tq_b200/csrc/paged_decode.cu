@@ -159,33 +159,34 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
 #pragma unroll
     for (int i = 0; i < PW / 8; ++i) srow[i] = src[i];
   }
-  for (int r = warp; r < R; r += DW) {
-    float x[NPL];
-    const int tok = (lo + r) / a.G, pos = sp.len - sp.n + tok;
-    const bool on = r < nrows && pos >= 0;
-    const int64_t off = (sp.row0 + tok) * a.st + (kvh * a.G + (lo + r) % a.G) * a.sh;
+  {
+    // warp w: rows w, w + 8, ..
+    float x[NT][NPL];
+    int64_t off[NT];
+    int at[NT];
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) x[k] = on ? tq_load_elem(a.q, off + lane + 32 * k, a.dtype) : 0.f;
-    if (a.rc != nullptr && on) {
+    for (int z = 0; z < NT; ++z) {
+      const int r = warp + DW * z, tok = (lo + r) / a.G;
+      at[z] = sp.len - sp.n + tok;
+      off[z] = r < nrows && at[z] >= 0
+                   ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + (lo + r) % a.G) * a.sh : -1;
+    }
+    paged_load_rows<NT, NPL>(x, a.q, off, a.dtype, lane);
+    paged_rope_rows<NT, NPL>(x, a.rc, a.rs, at, off, lane);
 #pragma unroll
-      for (int k = 0; k < NPL / 2; ++k) {
-        const float c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-        const float sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-        const float u = x[k], v = x[k + NPL / 2];
-        x[k] = u * c - v * sn;
-        x[k + NPL / 2] = v * c + u * sn;
+    for (int z = 0; z < NT; ++z) {
+      const int r = warp + DW * z;
+      if (a.books.pi != nullptr) {
+        tq_warp_dense<NPL>(x[z], a.books.pi_t, q1 + r * D, lane);
+      } else {
+        tq_apply_signs<NPL>(x[z], a.books.dneg, lane);
+        tq_warp_wht<NPL, true>(x[z], lane);
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) x[z][k] *= 1.0f / sqrtf(static_cast<float>(D));
       }
-    }
-    if (a.books.pi != nullptr) {
-      tq_warp_dense<NPL>(x, a.books.pi_t, q1 + r * D, lane);
-    } else {
-      tq_apply_signs<NPL>(x, a.books.dneg, lane);
-      tq_warp_wht<NPL>(x, lane);
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) x[k] *= 1.0f / sqrtf(static_cast<float>(D));
+      for (int k = 0; k < NPL; ++k) q1[r * D + lane + 32 * k] = x[z][k];
     }
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) q1[r * D + lane + 32 * k] = x[k];
   }
   __syncthreads();
   if (a.books.qjl) {

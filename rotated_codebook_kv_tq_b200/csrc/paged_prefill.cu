@@ -14,8 +14,14 @@
 //    accumulators in tensor memory, P = 2^(S 2^E + F - M) written over S as the
 //    fp16 operand.  Two query tiles alternate, so the products of one run under
 //    the softmax of the other.
-// Statistics and sums are fp32.  Roundings to fp16: q' scale log2 e, K^, V^ and
-// P, 2^-11 of an element each.
+// Statistics and sums are fp32.  Roundings to fp16: V^ (table entry and product) and
+// P, 2^-11 of an element each, which reach the answer directly; and in the logits, where
+// an error is multiplied by the logits' spread (ten and more where some channels are
+// large), only K^ at d = 128: queries are two fp16 terms, hi + lo, and at d = 64 the
+// keys too.  The extra products (S = (q_hi + q_lo) K^ is two, with K^_lo three) run
+// under the softmax: at d = 64 the exponentials alone take as long as all four
+// products, at d = 128 the three take 1.5 times as long, and a second key term would
+// not leave room for two tiles of queries and keys in shared memory.
 #include <math_constants.h>
 
 #include <cstdlib>
@@ -37,7 +43,9 @@ struct TileHeader {
   uint32_t there[4]; // bit per token
 };
 
-constexpr uint32_t tile_bytes(int d) { return HDR + 2u * TK * d * 2u; }
+constexpr uint32_t oper_bytes(int d) { return TK * d * 2u; }      // one operand tile
+constexpr bool key_lo(int d) { return d == 64; }                  // keys in two terms
+constexpr uint32_t tile_bytes(int d) { return HDR + (key_lo(d) ? 3u : 2u) * oper_bytes(d); }   // header, K^, (K^_lo,) V^
 
 struct PrefillArgs {
   PagedView p;
@@ -63,7 +71,7 @@ struct PrefillArgs {
   float *po;                 // [N Hq][splits][D]
   float2 *pml;
   uint32_t wait_outer;
-  uint32_t lutk[4], lutv[4];
+  uint32_t lutk[4], lutk_lo[4], lutv[4];
   TqBooks books;
 };
 
@@ -76,6 +84,30 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Operand layout: K-major with the 128-byte swizzle.  64 elements of K are a block of
+// rows x 128 bytes; the 16-byte chunk c of row r lies at chunk c ^ (r % 8) of its
+// 128 bytes.  (Slices of 16 bytes without the swizzle made a product of two shared
+// memory operands take 2400 cycles instead of 512.)
+__device__ __forceinline__ uint32_t swz(int rows, int r, int chunk) {
+  return (chunk >> 3) * rows * 128 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ uint64_t swz_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Descriptor of K elements 16 k .. 16 k + 15 of an operand of `rows` rows.
+__device__ __forceinline__ uint64_t swz_step(uint32_t addr, int rows, int k) {
+  return swz_desc(addr + (k >> 2) * rows * 128 + (k & 3) * 32);
+}
+
+// Two values as hi + lo pairs of fp16.
+__device__ __forceinline__ void split_half(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = pack_half(a - f.x, b - f.y);
 }
 
 // ------------------------------------------------------------------ expansion
@@ -232,28 +264,46 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
         fold_sign(w1);
       }
       // a thread's coordinates are places 32 t .. (d = 64: 16 t ..) of its rows
-      uint8_t *o = img + HDR + (D / 32) * t * (TK * 16) + 2 * warp * 128 + g * 16;
+      uint8_t *o = img + HDR;
+      const int n0r = 16 * warp + g, ch0 = (D / 32) * t;
 #pragma unroll
       for (int sft = 0; sft < 4; ++sft) {
-        uint32_t c0[4], c1[4];
-        expand8<K4>(nibbles<K4>(w0, sft), a.lutk, c0);
-        expand8<K4>(nibbles<K4>(w1, sft), a.lutk, c1);
+        uint32_t c0[4], c1[4], e0[4], e1[4];
+        const uint32_t n8 = nibbles<K4>(w0, sft), m8 = nibbles<K4>(w1, sft);
+        expand8<K4>(n8, a.lutk, c0);
+        expand8<K4>(m8, a.lutk, c1);
+        if (key_lo(D)) {
+          expand8<K4>(n8, a.lutk_lo, e0);
+          expand8<K4>(m8, a.lutk_lo, e1);
+        }
         constexpr int PR = D == 128 ? 4 : 2;      // pairs of a shift
-        uint32_t v0[PR], v1[PR];
+        uint32_t v0[PR], v1[PR], l0[PR], l1[PR];
 #pragma unroll
         for (int i = 0; i < PR; ++i) {
           const int n = PR * sft + i;
-          const float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&c0[i]));
-          const float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&c1[i]));
-          v0[i] = pack_half(n0 * fmaf(f0, acc[n][0], x0.x), n0 * fmaf(f0, acc[n][1], x0.y));
-          v1[i] = pack_half(n1 * fmaf(f1, acc[n][2], x1.x), n1 * fmaf(f1, acc[n][3], x1.y));
+          float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&c0[i]));
+          float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&c1[i]));
+          if (key_lo(D)) {
+            // the centroids' own second terms
+            const float2 y0 = __half22float2(*reinterpret_cast<const __half2 *>(&e0[i]));
+            const float2 y1 = __half22float2(*reinterpret_cast<const __half2 *>(&e1[i]));
+            split_half(n0 * fmaf(f0, acc[n][0], x0.x + y0.x), n0 * fmaf(f0, acc[n][1], x0.y + y0.y), v0[i], l0[i]);
+            split_half(n1 * fmaf(f1, acc[n][2], x1.x + y1.x), n1 * fmaf(f1, acc[n][3], x1.y + y1.y), v1[i], l1[i]);
+          } else {
+            v0[i] = pack_half(n0 * fmaf(f0, acc[n][0], x0.x), n0 * fmaf(f0, acc[n][1], x0.y));
+            v1[i] = pack_half(n1 * fmaf(f1, acc[n][2], x1.x), n1 * fmaf(f1, acc[n][3], x1.y));
+          }
         }
         if (D == 128) {
-          *reinterpret_cast<uint4 *>(o + sft * (TK * 16)) = make_uint4(v0[0], v0[1], v0[PR - 2], v0[PR - 1]);
-          *reinterpret_cast<uint4 *>(o + sft * (TK * 16) + 128) = make_uint4(v1[0], v1[1], v1[PR - 2], v1[PR - 1]);
+          *reinterpret_cast<uint4 *>(o + swz(TK, n0r, ch0 + sft)) = make_uint4(v0[0], v0[1], v0[PR - 2], v0[PR - 1]);
+          *reinterpret_cast<uint4 *>(o + swz(TK, n0r + 8, ch0 + sft)) = make_uint4(v1[0], v1[1], v1[PR - 2], v1[PR - 1]);
         } else {
-          *reinterpret_cast<uint2 *>(o + (sft >> 1) * (TK * 16) + 8 * (sft & 1)) = make_uint2(v0[0], v0[1]);
-          *reinterpret_cast<uint2 *>(o + (sft >> 1) * (TK * 16) + 8 * (sft & 1) + 128) = make_uint2(v1[0], v1[1]);
+          uint8_t *p = o + swz(TK, n0r, ch0 + (sft >> 1)) + 8 * (sft & 1);
+          uint8_t *q = o + swz(TK, n0r + 8, ch0 + (sft >> 1)) + 8 * (sft & 1);
+          *reinterpret_cast<uint2 *>(p) = make_uint2(v0[0], v0[1]);
+          *reinterpret_cast<uint2 *>(q) = make_uint2(v1[0], v1[1]);
+          *reinterpret_cast<uint2 *>(p + oper_bytes(D)) = make_uint2(l0[0], l0[1]);
+          *reinterpret_cast<uint2 *>(q + oper_bytes(D)) = make_uint2(l1[0], l1[1]);
         }
       }
     }
@@ -266,7 +316,7 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
 #pragma unroll
       for (int p = 0; p < 4; ++p) w[p] = on && p < nbv ? vw[p * D] : 0u;
       if (V4) fold_sign(w);
-      uint8_t *vimg = img + HDR + TK * D * 2 + (c >> 3) * 128 + (c & 7) * 16 + 4 * gr * (D * 16);
+      uint8_t *vimg = img + tile_bytes(D) - oper_bytes(D);
 #pragma unroll
       for (int sft = 0; sft < 4; ++sft) {
         uint32_t o[4];
@@ -278,7 +328,7 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
           const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&o[i]), *reinterpret_cast<const __half2 *>(&nw[i]));
           o[i] = *reinterpret_cast<const uint32_t *>(&r);
         }
-        *reinterpret_cast<uint4 *>(vimg + sft * (D * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(vimg + swz(D, c, 4 * gr + sft)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -286,15 +336,31 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
 
 // ------------------------------------------------------------------ attention
 
+// Shared memory: two query tiles in two terms, a ring of key tiles, a ring of
+// halves (64 tokens) of value tiles.  At d = 128 one value tile fits: its halves are
+// refilled as soon as the last product over them has run.
 template <int D>
 struct Smem {
-  static constexpr int STG = D == 128 ? 2 : 4;
-  static constexpr uint32_t OPER = TK * D * 2;   // one operand tile
-  static constexpr uint32_t Q = 0, K = 2 * OPER, V = K + STG * OPER, END = V + STG * OPER;
+  static constexpr int KT = key_lo(D) ? 2 : 1;        // key terms
+  static constexpr int SK = D == 128 ? 2 : 3;         // key tiles
+  static constexpr int SV = D == 128 ? 2 : 6;         // value halves
+  static constexpr uint32_t OPER = oper_bytes(D), VH = OPER / 2;
+  static constexpr uint32_t Q = 0, K = 4 * OPER, V = K + SK * KT * OPER, END = V + SV * VH;
 };
 
+__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(sm100::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // Bounded wait that gives up as soon as another thread has.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint32_t outer, volatile int *abort_flag) {
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, uint32_t outer, volatile int *abort_flag) {
+#pragma unroll 1
   for (uint32_t it = 0; it < outer; ++it) {
     if (sm100::mbar_wait(bar, parity, 1u << 14)) return true;
     if (*abort_flag) return false;
@@ -302,13 +368,47 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint32_
   *abort_flag = 1;
   return false;
 }
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint32_t outer, volatile int *abort_flag) {
+  if (outer > 0 && try_phase(bar, parity)) return true;
+  return wait_slow(bar, parity, outer, abort_flag);
+}
 
+// The same by a whole warp, with one answer; lanes may wait on different barriers.
+__device__ __forceinline__ bool warp_wait_for(uint64_t *bar, uint32_t parity, uint32_t outer, volatile int *abort_flag) {
+  const bool ok = outer > 0 && try_phase(bar, parity);
+  if (__all_sync(TQ_FULL, ok)) return true;
+  return __all_sync(TQ_FULL, ok || wait_slow(bar, parity, outer, abort_flag));
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+
+// 12 warps: 0-3 and 4-7 the softmax of the two query tiles, 8 the products, 9
+// the copies (10 and 11 fill their warpgroup, which hands its registers on).
 template <int D>
-__global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_constant__ PrefillArgs a) {
+__global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   using L = Smem<D>;
-  constexpr int NPL = D / 32, STG = L::STG;
-  extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ __align__(8) uint64_t kfull[STG], kempty[STG], vfull[STG], vempty[STG], sfull[2], pfull[2], ofull[2],
+  constexpr int NPL = D / 32, SK = L::SK, SV = L::SV;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ __align__(8) uint64_t kfull[SK], kempty[SK], vfull[SV], vempty[SV], sfull[2], pfull[2], ofull[2], qfull,
       fin;
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
@@ -324,22 +424,24 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
   if (u < 0 || tok0 >= sp.n) return;
   const int pos0 = sp.len - sp.n;          // position of new token 0
   // token tiles of the two query tiles, and of this block
-  int vis[2], k1[2];
+  const int k0 = split * a.chunk;
+  int nx[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int first = tok0 + x * a.tok_tile, last = min(first + a.tok_tile, sp.n) - 1;
-    vis[x] = first < sp.n ? max(0, min(sp.len, pos0 + last + 1)) : 0;
-    k1[x] = min((vis[x] + TK - 1) / TK, (split + 1) * a.chunk);
+    const int vis = first < sp.n ? max(0, min(sp.len, pos0 + last + 1)) : 0;
+    nx[x] = max(0, min((vis + TK - 1) / TK, (split + 1) * a.chunk) - k0);
   }
-  const int k0 = split * a.chunk;
-  const int nA = max(0, k1[0] - k0), nB = max(0, k1[1] - k0), n = max(nA, nB);
+  const int n = max(nx[0], nx[1]);
   if (n == 0 && split > 0) return;
 
   if (warp == 8) sm100::tmem_alloc(&tmem_s, 512);
   if (tid == 0) {
-    for (int i = 0; i < STG; ++i) {
+    for (int i = 0; i < SK; ++i) {
       sm100::mbar_init(&kfull[i], 1);
       sm100::mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < SV; ++i) {
       sm100::mbar_init(&vfull[i], 1);
       sm100::mbar_init(&vempty[i], 1);
     }
@@ -348,171 +450,210 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
       sm100::mbar_init(&pfull[i], TQ);
       sm100::mbar_init(&ofull[i], 1);
     }
+    sm100::mbar_init(&qfull, 2 * TQ);
     sm100::mbar_init(&fin, 1);
     abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const uint8_t *img0 = a.tiles + (static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles * tile_bytes(D);
-  // ---- query operands: warp w of a tile's four prepares rows 32 w .. 32 w + 31
-  if (warp < 8) {
-    const int x = warp >> 2;
-    uint8_t *qimg = sm + L::Q + x * L::OPER;
-    constexpr int QB = 4;       // rows in flight
-#pragma unroll 1
-    for (int rb = 32 * (warp & 3); rb < 32 * (warp & 3) + 32; rb += QB) {
-      float v[QB][NPL], cs[QB][NPL / 2], sn[QB][NPL / 2];
-#pragma unroll
-      for (int z = 0; z < QB; ++z) {
-        const int r = rb + z, tt = r / a.G, tok = tok0 + x * a.tok_tile + tt, pos = pos0 + tok;
-        const bool on = tt < a.tok_tile && tok < sp.n && pos >= 0;
-        const int64_t off = static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + r % a.G) * a.sh;
-#pragma unroll
-        for (int k = 0; k < NPL; ++k) v[z][k] = on ? tq_load_elem(a.q, off + lane + 32 * k, a.dtype) : 0.f;
-#pragma unroll
-        for (int k = 0; k < NPL / 2; ++k) {
-          const bool rope = a.rc != nullptr && on;
-          cs[z][k] = rope ? a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k] : 1.f;
-          sn[z][k] = rope ? a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int z = 0; z < QB; ++z) {
-        const int r = rb + z;
-#pragma unroll
-        for (int k = 0; k < NPL / 2; ++k) {
-          const float p = v[z][k], w = v[z][k + NPL / 2];
-          v[z][k] = p * cs[z][k] - w * sn[z][k];
-          v[z][k + NPL / 2] = w * cs[z][k] + p * sn[z][k];
-        }
-        float f = a.scale * 1.4426950408889634f;
-        if (a.books.pi != nullptr) {
-          // the value operands' place holds no tile yet
-          tq_warp_dense<NPL>(v[z], a.books.pi_t, reinterpret_cast<float *>(sm + L::V) + warp * D, lane);
-        } else {
-          tq_apply_signs<NPL>(v[z], a.books.dneg, lane);
-          tq_warp_wht<NPL, true>(v[z], lane);
-          f *= 1.0f / sqrtf(static_cast<float>(D));
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < NPL; ++k) {
-          v[z][k] *= f;
-          m = fmaxf(m, fabsf(v[z][k]));
-        }
-        m = tq_warp_max(m);
-        // a power of two taken out where fp16 would lose digits or overflow
-        const int e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-120, min(120, ilogbf(m) + 1)) : 0;
-#pragma unroll
-        for (int k = 0; k < NPL; ++k) {
-          const int c = coord_place<D>(lane + 32 * k);
-          *reinterpret_cast<__half *>(qimg + (c >> 3) * (TQ * 16) + (r >> 3) * 128 + (r & 7) * 16 + (c & 7) * 2) =
-              __float2half_rn(e == 0 ? v[z][k] : ldexpf(v[z][k], -e));
-        }
-        if (lane == 0) frow[x][r] = ldexpf(1.f, e);
-      }
-    }
-    sm100::fence_async_smem();
-  }
+  const uint8_t *img0 = a.tiles + (static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles * tile_bytes(D) +
+                        static_cast<int64_t>(k0) * tile_bytes(D);
   sm100::fence_before_sync();
   __syncthreads();
   sm100::fence_after_sync();
   const uint32_t tm = tmem_s;
 
-  if (warp == 9) {
-    // ---- copies
-    if (lane == 0) {
-      int kc = 0, vc = 0;     // tiles copied so far
-      for (int i = 0; i < n; ++i) {
-        const int st = i % STG;
-        const uint8_t *img = img0 + static_cast<int64_t>(k0 + i) * tile_bytes(D);
-        if (i >= STG && !wait_for(&kempty[st], (i / STG - 1) & 1, a.wait_outer, &abort_s)) break;
-        sm100::mbar_expect_tx(&kfull[st], L::OPER);
-        sm100::bulk_g2s(sm + L::K + st * L::OPER, img + HDR, L::OPER, &kfull[st]);
+  // 384 threads at 168 registers: 256 x 216 + 128 x 72 is the same total
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 9 && lane == 0) {
+      // ---- copies
+      int kc = 0, vc = 0;     // key tiles, value halves copied so far
+      bool ok = true;
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i % SK;
+        const uint8_t *img = img0 + static_cast<int64_t>(i) * tile_bytes(D) + HDR;
+        ok = i < SK || wait_for(&kempty[st], (i / SK - 1) & 1, a.wait_outer, &abort_s);
+        if (!ok) break;
+        sm100::mbar_expect_tx(&kfull[st], L::KT * L::OPER);
+        sm100::bulk_g2s(sm + L::K + st * L::KT * L::OPER, img, L::KT * L::OPER, &kfull[st]);
         ++kc;
-        if (i >= STG && !wait_for(&vempty[st], (i / STG - 1) & 1, a.wait_outer, &abort_s)) break;
-        sm100::mbar_expect_tx(&vfull[st], L::OPER);
-        sm100::bulk_g2s(sm + L::V + st * L::OPER, img + HDR + L::OPER, L::OPER, &vfull[st]);
-        ++vc;
+        for (int q = 0; q < 2; ++q) {
+          const int vs = vc % SV;
+          ok = vc < SV || wait_for(&vempty[vs], (vc / SV - 1) & 1, a.wait_outer, &abort_s);
+          if (!ok) break;
+          sm100::mbar_expect_tx(&vfull[vs], L::VH);
+          sm100::bulk_g2s(sm + L::V + vs * L::VH, img + L::KT * L::OPER + q * L::VH, L::VH, &vfull[vs]);
+          ++vc;
+        }
       }
       // nothing may be in flight when the block's shared memory is released:
       // the last copy of every slot has landed
-      for (int i = max(0, kc - STG); i < kc; ++i) sm100::mbar_wait(&kfull[i % STG], (i / STG) & 1, 1u << 24);
-      for (int i = max(0, vc - STG); i < vc; ++i) sm100::mbar_wait(&vfull[i % STG], (i / STG) & 1, 1u << 24);
-    }
-    __syncwarp();
-  } else if (warp == 8) {
-    // ---- products, issued by one thread
-    if (lane == 0) {
+      for (int i = max(0, kc - SK); i < kc; ++i) sm100::mbar_wait(&kfull[i % SK], (i / SK) & 1, 1u << 24);
+      for (int i = max(0, vc - SV); i < vc; ++i) sm100::mbar_wait(&vfull[i % SV], (i / SV) & 1, 1u << 24);
+    } else if (warp == 8) {
+      // ---- products, issued by one elected lane (the same one each time)
       constexpr uint32_t ID_S = sm100::idesc_f16(TQ, TK), ID_O = sm100::idesc_f16(TQ, D);
       const uint32_t aq = sm100::smem_addr(sm + L::Q), ak = sm100::smem_addr(sm + L::K),
                      av = sm100::smem_addr(sm + L::V);
+      // S = q_lo K + (q_hi K_lo) + q_hi K: the small products first
       auto s_mma = [&](int x, int st) {
+        uint32_t acc = 0u;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          sm100::mma_bf16_ss(tm + x * 128, sm100::smem_desc(aq + x * L::OPER + k * 2 * (TQ * 16), TQ * 16, 128),
-                             sm100::smem_desc(ak + st * L::OPER + k * 2 * (TK * 16), TK * 16, 128), ID_S,
-                             k > 0 ? 1u : 0u);
-      };
-      auto o_mma = [&](int x, int st, bool first) {
+        for (int t = L::KT; t >= 0; --t) {
+          const uint32_t qo = aq + (2 * x + (t == 1)) * L::OPER, ko = ak + (st * L::KT + (t == 2)) * L::OPER;
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
-          sm100::mma_f16_ts(tm + 256 + x * D, tm + x * 128 + k * 8,
-                            sm100::smem_desc(av + st * L::OPER + k * 2 * (D * 16), D * 16, 128), ID_O,
-                            (k > 0 || !first) ? 1u : 0u);
-      };
-      const int nx[2] = {nA, nB};
-      bool ok = n > 0 && wait_for(&kfull[0], 0, a.wait_outer, &abort_s);
-      if (ok) {
-        for (int x = 0; x < 2; ++x)
-          if (nx[x] > 0) {
-            s_mma(x, 0);
-            sm100::mma_commit(&sfull[x]);
-          }
-        sm100::mma_commit(&kempty[0]);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        const int st = i % STG, st1 = (i + 1) % STG;
-        if (i + 1 < n) ok = wait_for(&kfull[st1], ((i + 1) / STG) & 1, a.wait_outer, &abort_s);
-        ok = ok && wait_for(&vfull[st], (i / STG) & 1, a.wait_outer, &abort_s);
-        for (int x = 0; ok && x < 2; ++x) {
-          if (i >= nx[x]) continue;
-          ok = wait_for(&pfull[x], i & 1, a.wait_outer, &abort_s);
-          if (!ok) break;
-          sm100::fence_after_sync();
-          o_mma(x, st, i == 0);
-          if (i + 1 < nx[x]) {
-            s_mma(x, st1);
-            sm100::mma_commit(&sfull[x]);
-          } else {
-            sm100::mma_commit(&ofull[x]);
+          for (int k = 0; k < D / 16; ++k) {
+            sm100::warp_mma_f16_ss(tm + x * 128, swz_step(qo, TQ, k), swz_step(ko, TK, k), ID_S, acc);
+            acc = 1u;
           }
         }
-        sm100::mma_commit(&vempty[st]);
-        if (i + 1 < n) sm100::mma_commit(&kempty[st1]);
+        sm100::warp_mma_commit(&sfull[x]);
+      };
+      bool ok = warp_wait_for(&qfull, 0, a.wait_outer, &abort_s);
+      ok = ok && n > 0 && warp_wait_for(&kfull[0], 0, a.wait_outer, &abort_s);
+      if (ok) {
+        for (int x = 0; x < 2; ++x)
+          if (nx[x] > 0) s_mma(x, 0);
+        sm100::warp_mma_commit(&kempty[0]);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int st1 = (i + 1) % SK, vq = 2 * i, v0 = vq % SV, v1 = (vq + 1) % SV;
+        // the query tiles that read this value tile
+        const int lastx = i < nx[1] ? 1 : 0, firstx = i < nx[0] ? 0 : 1;
+        // one wait for all that the iteration's first products need, a barrier a lane
+        // (a wait on a phase that is over still takes a few hundred cycles)
+        {
+          uint64_t *bar = lane == 1 ? &vfull[v0] : lane == 2 ? &vfull[v1] : lane == 3 && i + 1 < n ? &kfull[st1] : &pfull[firstx];
+          const uint32_t par = lane == 1 ? (vq / SV) & 1 : lane == 2 ? ((vq + 1) / SV) & 1
+                                         : lane == 3 && i + 1 < n ? ((i + 1) / SK) & 1 : i & 1;
+          ok = warp_wait_for(bar, par, a.wait_outer, &abort_s);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || i >= nx[x]) continue;
+          if (x != firstx) ok = warp_wait_for(&pfull[x], i & 1, a.wait_outer, &abort_s);
+          if (!ok) continue;
+          sm100::fence_after_sync();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int vs = q ? v1 : v0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sm100::warp_mma_f16_ts(tm + 256 + x * D, tm + x * 128 + (4 * q + k) * 8, swz_step(av + vs * L::VH, D, k),
+                                     ID_O, (i > 0 || q + k > 0) ? 1u : 0u);
+            if (x == lastx) sm100::warp_mma_commit(&vempty[vs]);
+          }
+          if (i + 1 < nx[x])
+            s_mma(x, st1);
+          else
+            sm100::warp_mma_commit(&ofull[x]);
+        }
+        if (ok && i + 1 < n) sm100::warp_mma_commit(&kempty[st1]);
       }
       // every product has landed before tensor memory is released
-      sm100::mma_commit(&fin);
+      sm100::warp_mma_commit(&fin);
       sm100::mbar_wait(&fin, 0, 1u << 24);
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int x = warp >> 2, lq = warp & 3;
+    // ---- query operands: warp lq of a tile prepares its rows 32 lq .. 32 lq + 31
+    {
+      constexpr int QB = D == 128 ? 4 : 8;       // rows in flight
+      uint8_t *qimg = sm + L::Q + x * 2 * L::OPER;
+      int tt = 32 * lq / a.G, gh = 32 * lq % a.G;    // token of the tile, head of the group
+#pragma unroll 1
+      for (int rb = 32 * lq; rb < 32 * lq + 32; rb += QB) {
+        float v[QB][NPL];
+        int64_t off[QB];
+        int at[QB];
+#pragma unroll
+        for (int z = 0; z < QB; ++z) {
+          const int tok = tok0 + x * a.tok_tile + tt;
+          at[z] = pos0 + tok;
+          const bool on = tt < a.tok_tile && tok < sp.n && at[z] >= 0;
+          off[z] = on ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + gh) * a.sh : -1;
+          if (++gh == a.G) {
+            gh = 0;
+            ++tt;
+          }
+        }
+        paged_load_rows<QB, NPL>(v, a.q, off, a.dtype, lane);
+        paged_rope_rows<QB, NPL>(v, a.rc, a.rs, at, off, lane);
+        float f = a.scale * 1.4426950408889634f;
+        if (a.books.pi != nullptr) {
+          // scratch: d floats of this warp's second-term rows, none of which is
+          // written before its batch has been rotated (the last rows' are taken)
+          float *scr = reinterpret_cast<float *>(qimg + L::OPER + (32 * lq + 32) * 128) - D;
+#pragma unroll
+          for (int z = 0; z < QB; ++z) tq_warp_dense<NPL>(v[z], a.books.pi_t, scr, lane);
+        } else {
+#pragma unroll
+          for (int z = 0; z < QB; ++z) {
+            tq_apply_signs<NPL>(v[z], a.books.dneg, lane);
+            tq_warp_wht<NPL, true>(v[z], lane);
+          }
+          f *= 1.0f / sqrtf(static_cast<float>(D));
+        }
+#pragma unroll
+        for (int z = 0; z < QB; ++z) {
+          const int r = rb + z;
+          float m = 0.f;
+#pragma unroll
+          for (int k = 0; k < NPL; ++k) {
+            v[z][k] *= f;
+            m = fmaxf(m, fabsf(v[z][k]));
+          }
+          m = tq_warp_max(m);
+          // a power of two 2^e taken out where fp16 would lose digits or overflow
+          // (between 2^-100 and 2^100)
+          int e = static_cast<int>(__float_as_uint(m) >> 23) - 126;
+          e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-100, min(100, e)) : 0;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+          for (int k = 0; k < NPL; ++k) {
+            const int c = coord_place<D>(lane + 32 * k);
+            const float w = v[z][k] * down;
+            const __half hi = __float2half_rn(w);
+            uint8_t *dst = qimg + swz(TQ, r, c >> 3) + (c & 7) * 2;
+            *reinterpret_cast<__half *>(dst) = hi;
+            *reinterpret_cast<__half *>(dst + L::OPER) = __float2half_rn(w - __half2float(hi));
+          }
+          if (lane == 0) frow[x][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        }
+      }
+      sm100::fence_async_smem();
+      __syncwarp();
+      sm100::mbar_arrive(&qfull);
+    }
     // ---- softmax: a thread a query row
-    const int x = warp >> 2, r = tid & (TQ - 1), lq = warp & 3;
+    const int r = tid & (TQ - 1);
     const int tt = r / a.G, tok = tok0 + x * a.tok_tile + tt;
     const bool live = tt < a.tok_tile && tok < sp.n;
     const int pos = live ? pos0 + tok : -1;
     const int pos_min = pos0 + tok0 + x * a.tok_tile;       // smallest of the tile
     const float f = frow[x][r];
-    const int nx = x ? nB : nA;
+    const int nt = x ? nx[1] : nx[0];
     const uint32_t tS = sm100::tmem_lane(tm + x * 128, lq), tO = sm100::tmem_lane(tm + 256 + x * D, lq);
     float M = -1e30f, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < nx; ++i) {
-      const TileHeader *hd =
-          reinterpret_cast<const TileHeader *>(img0 + static_cast<int64_t>(k0 + i) * tile_bytes(D));
-      const float F = hd->k_exp * f, ve = hd->v_exp, vi = hd->v_inv;
+    // the header of a tile, fetched a tile ahead
+    float4 next = make_float4(1.f, 0.f, 1.f, 0.f);
+    uint4 bits = make_uint4(0u, 0u, 0u, 0u);
+    if (nt > 0) {
+      next = *reinterpret_cast<const float4 *>(img0);
+      bits = *reinterpret_cast<const uint4 *>(img0 + 16);
+    }
+    for (int i = 0; i < nt; ++i) {
+      const uint32_t there[4] = {bits.x, bits.y, bits.z, bits.w};
+      const float F = next.x * f, ve = next.y, vi = next.z;
       const int j0 = (k0 + i) * TK;
-      const bool masked = !hd->all || j0 + TK - 1 > pos_min;
+      const bool masked = __float_as_uint(next.w) == 0u || j0 + TK - 1 > pos_min;
+      if (i + 1 < nt) {
+        next = *reinterpret_cast<const float4 *>(img0 + static_cast<int64_t>(i + 1) * tile_bytes(D));
+        bits = *reinterpret_cast<const uint4 *>(img0 + static_cast<int64_t>(i + 1) * tile_bytes(D) + 16);
+      }
       ok = wait_for(&sfull[x], i & 1, a.wait_outer, &abort_s);
       if (!__all_sync(TQ_FULL, ok)) break;
       sm100::fence_after_sync();
@@ -524,18 +665,25 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int lim = pos - (j0 + 32 * c);      // last visible of these 32
-          const uint32_t see = hd->there[c] & (lim < 0 ? 0u : lim >= 31 ? ~0u : (2u << lim) - 1u);
+          const uint32_t see = there[c] & (lim < 0 ? 0u : lim >= 31 ? ~0u : (2u << lim) - 1u);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!((see >> place_token(e)) & 1u)) sv[c][e] = 0xff800000u;
         }
       }
-      float mx = -CUDART_INF_F;
+      float mx[8];      // eight chains
+#pragma unroll
+      for (int z = 0; z < 8; ++z) mx[z] = -CUDART_INF_F;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[c][e]));
-      const float top = fmaf(mx, F, ve);
+        for (int e = 0; e < 32; e += 16)
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(sv[c][e + z]), __uint_as_float(sv[c][e + 8 + z])));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], mx[e + 4]);
+      const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), F, ve);
       // the reference moves only when a weight would exceed 2^8
       if (__any_sync(TQ_FULL, top > M + 8.f)) {
         const float mn = fmaxf(M, top), corr = ex2(M - mn);
@@ -543,36 +691,38 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
         l *= corr;
         if (i > 0) {
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            sm100::tmem_ld32(tO + c, o);
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            sm100::tmem_ld8(tO + c, o);
             sm100::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            sm100::tmem_st32(tO + c, o);
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            sm100::tmem_st8(tO + c, o);
           }
         }
       }
-      const float off = ve - M;
-      float sum = 0.f;
+      const uint64_t F2 = pair(F, F), off2 = pair(ve - M, ve - M);
+      uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t pw[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(sv[2 * c + (e >> 4)][(2 * e) & 31]), F, off));
-          const float p1 = ex2(fmaf(__uint_as_float(sv[2 * c + (e >> 4)][(2 * e + 1) & 31]), F, off));
-          sum += p0 + p1;
+          const uint32_t *v = &sv[2 * c + (e >> 4)][(2 * e) & 31];
+          const float2 t = unpair(fma2(pair(__uint_as_float(v[0]), __uint_as_float(v[1])), F2, off2));
+          const float p0 = ex2(t.x), p1 = ex2(t.y);
+          sum2[e & 3] = add2(sum2[e & 3], pair(p0, p1));
           pw[e] = pack_half(p0, p1);
         }
         sm100::tmem_st32(tS + 32 * c, pw);
       }
-      l = fmaf(sum, vi, l);
       sm100::wait_st();
       sm100::fence_before_sync();
       sm100::mbar_arrive(&pfull[x]);
+      const float2 sum = unpair(add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3])));
+      l = fmaf(sum.x + sum.y, vi, l);
     }
-    if (ok && nx > 0) ok = wait_for(&ofull[x], 0, a.wait_outer, &abort_s);
+    if (ok && nt > 0) ok = wait_for(&ofull[x], 0, a.wait_outer, &abort_s);
     ok = __all_sync(TQ_FULL, ok);
     sm100::fence_after_sync();
     float o[D];
@@ -582,12 +732,12 @@ __global__ void __launch_bounds__(320, 1) paged_prefill_kernel(const __grid_cons
       sm100::tmem_ld32(tO + c, w);
       sm100::wait_ld();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[c + e] = nx > 0 ? __uint_as_float(w[e]) : 0.f;
+      for (int e = 0; e < 32; ++e) o[c + e] = nt > 0 ? __uint_as_float(w[e]) : 0.f;
     }
     if (!ok) l = CUDART_NAN_F;    // a wait ran out: the rows are answered with NaN
     const int64_t row = static_cast<int64_t>(sp.row0 + tok) * a.Hq + kvh * a.G + r % a.G;
     // a split past the row's tiles writes nothing, and the join reads nothing
-    if (live && a.splits > 1 && (split == 0 || nx > 0)) {
+    if (live && a.splits > 1 && (split == 0 || nt > 0)) {
       float4 *dst = reinterpret_cast<float4 *>(a.po + (row * a.splits + split) * D);
 #pragma unroll
       for (int c = 0; c < D; c += 4) dst[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
@@ -720,7 +870,7 @@ int run_prefill(PrefillArgs &a, const Plan &pl, bool k4, bool v4, cudaStream_t s
                  : (v4 ? paged_expand_kernel<D, false, true> : paged_expand_kernel<D, false, false>);
     ex<<<static_cast<unsigned>(std::min<int64_t>(items, 2 * 148)), 256, es, stream>>>(a);
     if (int e = tq_check_launch("paged_expand_kernel")) return e;
-    paged_prefill_kernel<D><<<dim3(pl.units, a.heads, pl.splits), 320, shm, stream>>>(a);
+    paged_prefill_kernel<D><<<dim3(pl.units, a.heads, pl.splits), 384, shm, stream>>>(a);
     if (int e = tq_check_launch("paged_prefill_kernel")) return e;
     tq_count_launch(2);
     if (pl.splits > 1) {
@@ -776,6 +926,9 @@ int launch_paged_prefill(const tq_codec *c, const PagedView &p, const void *q, i
     a.wait_outer = static_cast<uint32_t>((strtoul(e, nullptr, 10) + (1u << 14) - 1) >> 14);
   a.books = c->books;
   byte_table(c->books.ck, c->mse_bits_k, a.lutk);
+  float lo[TQ_MAX_LEVELS];
+  for (int i = 0; i < TQ_MAX_LEVELS; ++i) lo[i] = c->books.ck[i] - __half2float(__float2half_rn(c->books.ck[i]));
+  byte_table(lo, c->mse_bits_k, a.lutk_lo);
   byte_table(c->books.cv, c->bits_v, a.lutv);
   const bool k4 = c->mse_bits_k == 4, v4 = c->bits_v == 4;
   return c->d == 64 ? run_prefill<64>(a, pl, k4, v4, stream) : run_prefill<128>(a, pl, k4, v4, stream);

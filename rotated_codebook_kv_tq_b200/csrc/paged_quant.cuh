@@ -94,8 +94,11 @@ template <int NPL>
 __device__ __forceinline__ void load_f64(double (&x)[NPL], const void *base, int64_t off, int dtype, const float *rc,
                                          const float *rs, int64_t pos, int lane) {
   constexpr int D = NPL * 32;
+  float f[1][NPL];
+  const int64_t offs[1] = {off};
+  paged_load_rows<1, NPL>(f, base, offs, dtype, lane);
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(base, off + lane + 32 * k, dtype);
+  for (int k = 0; k < NPL; ++k) x[k] = f[0][k];
   if (rc != nullptr) {
 #pragma unroll
     for (int k = 0; k < NPL / 2; ++k) {

@@ -106,20 +106,13 @@ __global__ void __launch_bounds__(128) paged_quantize_kernel(const __grid_consta
   uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + row * planes * (D / 8));
   sm100::pdl_trigger();
   if (warp < 2) {
-    float x[NPL];
+    float xr[1][NPL];
+    float (&x)[NPL] = xr[0];
     const void *src = warp == 0 ? a.k : a.v;
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) x[k] = tq_load_elem(src, off + lane + 32 * k, a.dtype);
-    if (warp == 0 && a.rc != nullptr) {
-#pragma unroll
-      for (int k = 0; k < NPL / 2; ++k) {
-        const float c = a.rc[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-        const float sn = a.rs[static_cast<int64_t>(pos) * (D / 2) + lane + 32 * k];
-        const float u = x[k], w = x[k + NPL / 2];
-        x[k] = u * c - w * sn;
-        x[k + NPL / 2] = w * c + u * sn;
-      }
-    }
+    const int64_t offs[1] = {off};
+    const int poss[1] = {pos};
+    paged_load_rows<1, NPL>(xr, src, offs, a.dtype, lane);
+    if (warp == 0) paged_rope_rows<1, NPL>(xr, a.rc, a.rs, poss, offs, lane);
     bool bad, again;
     float nu = unit_f32<NPL>(x, a.books, fscr[warp], lane, bad, again);
     int idx[NPL];
