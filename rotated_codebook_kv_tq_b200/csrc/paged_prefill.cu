@@ -97,10 +97,7 @@ __device__ __forceinline__ uint64_t swz_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// Descriptor of K elements 16 k .. 16 k + 15 of an operand of `rows` rows.
-__device__ __forceinline__ uint64_t swz_step(uint32_t addr, int rows, int k) {
-  return swz_desc(addr + (k >> 2) * rows * 128 + (k & 3) * 32);
-}
+// (K elements 16 k .. 16 k + 15 start (k / 4) rows x 128 + (k % 4) 32 bytes further.)
 
 // Two values as hi + lo pairs of fp16.
 __device__ __forceinline__ void split_half(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -497,23 +494,29 @@ __global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_cons
                      av = sm100::smem_addr(sm + L::V);
       // S = q_lo K + (q_hi K_lo) + q_hi K: the small products first
       auto s_mma = [&](int x, int st) {
+        // (loops kept rolled: every block runs this code a few times only, and what it
+        // costs then is fetching it)
         uint32_t acc = 0u;
-#pragma unroll
+#pragma unroll 1
         for (int t = L::KT; t >= 0; --t) {
-          const uint32_t qo = aq + (2 * x + (t == 1)) * L::OPER, ko = ak + (st * L::KT + (t == 2)) * L::OPER;
+          const uint64_t q0 = swz_desc(aq + (2 * x + (t == 1)) * L::OPER), d0 = swz_desc(ak + (st * L::KT + (t == 2)) * L::OPER);
+#pragma unroll 1
+          for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            sm100::warp_mma_f16_ss(tm + x * 128, swz_step(qo, TQ, k), swz_step(ko, TK, k), ID_S, acc);
-            acc = 1u;
-          }
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t step = (b * TQ * 128 + k * 32) >> 4;
+              sm100::warp_mma_f16_ss(tm + x * 128, q0 + step, d0 + step, ID_S, acc);
+              acc = 1u;
+            }
         }
         sm100::warp_mma_commit(&sfull[x]);
       };
       bool ok = warp_wait_for(&qfull, 0, a.wait_outer, &abort_s);
       ok = ok && n > 0 && warp_wait_for(&kfull[0], 0, a.wait_outer, &abort_s);
       if (ok) {
+#pragma unroll 1
         for (int x = 0; x < 2; ++x)
-          if (nx[x] > 0) s_mma(x, 0);
+          if ((x ? nx[1] : nx[0]) > 0) s_mma(x, 0);
         sm100::warp_mma_commit(&kempty[0]);
       }
       for (int i = 0; ok && i < n; ++i) {
@@ -528,22 +531,24 @@ __global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_cons
                                          : lane == 3 && i + 1 < n ? ((i + 1) / SK) & 1 : i & 1;
           ok = warp_wait_for(bar, par, a.wait_outer, &abort_s);
         }
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          if (!ok || i >= nx[x]) continue;
+          const int nxx = x ? nx[1] : nx[0];
+          if (!ok || i >= nxx) continue;
           if (x != firstx) ok = warp_wait_for(&pfull[x], i & 1, a.wait_outer, &abort_s);
           if (!ok) continue;
           sm100::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             const int vs = q ? v1 : v0;
+            const uint64_t d0 = swz_desc(av + vs * L::VH);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              sm100::warp_mma_f16_ts(tm + 256 + x * D, tm + x * 128 + (4 * q + k) * 8, swz_step(av + vs * L::VH, D, k),
-                                     ID_O, (i > 0 || q + k > 0) ? 1u : 0u);
+              sm100::warp_mma_f16_ts(tm + 256 + x * D, tm + x * 128 + (4 * q + k) * 8, d0 + ((k * 32) >> 4), ID_O,
+                                     (i > 0 || q + k > 0) ? 1u : 0u);
             if (x == lastx) sm100::warp_mma_commit(&vempty[vs]);
           }
-          if (i + 1 < nx[x])
+          if (i + 1 < nxx)
             s_mma(x, st1);
           else
             sm100::warp_mma_commit(&ofull[x]);
