@@ -71,6 +71,7 @@ struct PrefillArgs {
   float *po;                 // [N Hq][splits][D]
   float2 *pml;
   uint32_t wait_outer;
+  bool q_vec, rope_vec;      // 16-byte loads fit
   uint32_t lutk[4], lutk_lo[4], lutv[4];
   TqBooks books;
 };
@@ -398,12 +399,134 @@ __device__ __forceinline__ float2 unpair(uint64_t a) {
   return r;
 }
 
+__device__ __forceinline__ void load_table_row(float (&v)[8], const float *p, bool vec) {
+  if (vec) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __ldg(p + e);
+  }
+}
+__device__ __forceinline__ void load_table(float (&v)[2][8], const float *p, const float *q, bool vec) {
+  load_table_row(v[0], p, vec);
+  load_table_row(v[1], q, vec);
+}
+
+// Coordinates 8 j .. 8 j + 7 of both halves of a row (off: the first one's element
+// offset, negative for a row of zeros); vec: 16-byte loads fit.
+template <int D>
+__device__ __forceinline__ void load_halves(float (&v)[2][8], const void *base, int64_t off, int dtype, bool vec) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[h][e] = 0.f;
+  if (off < 0) return;
+  if (dtype == TQ_BF16) {
+    const uint16_t *p = static_cast<const uint16_t *>(base) + off;
+    uint32_t w[2][4];
+    if (vec) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + h * (D / 2)));
+        w[h][0] = u.x;
+        w[h][1] = u.y;
+        w[h][2] = u.z;
+        w[h][3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[h][e] = p[h * (D / 2) + 2 * e] | (static_cast<uint32_t>(p[h * (D / 2) + 2 * e + 1]) << 16);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[h][2 * e] = __uint_as_float(w[h][e] << 16);
+        v[h][2 * e + 1] = __uint_as_float(w[h][e] & 0xffff0000u);
+      }
+  } else {
+    const float *p = static_cast<const float *>(base) + off;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_table_row(v[h], p + h * (D / 2), vec);
+  }
+}
+
+// The randomized Walsh-Hadamard transform (without its 1 / sqrt(d)) of rows held by
+// D / 16 lanes each, coordinates 8 j + e and d / 2 + 8 j + e in v[0][e] and v[1][e].
+template <int D>
+__device__ __forceinline__ void rotate_hadamard(float (&v)[2][8], const uint32_t *dneg, int j) {
+  constexpr int LPR = D / 16;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = 8 * j + h * (D / 2);
+    const uint32_t neg = dneg[c >> 5] >> (c & 31);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[h][e] = __uint_as_float(__float_as_uint(v[h][e]) ^ ((neg >> e) << 31));
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(e & s)) {
+          const float a = v[h][e], b = v[h][e + s];
+          v[h][e] = a + b;
+          v[h][e + s] = a - b;
+        }
+  }
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1) {
+    const float sg = j & o ? -1.f : 1.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[h][e] = fmaf(sg, v[h][e], __shfl_xor_sync(TQ_FULL, v[h][e], o));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = v[0][e], b = v[1][e];
+    v[0][e] = a + b;
+    v[1][e] = a - b;
+  }
+}
+
+// The same with a dense rotation (pi_t[j d + i] = Pi_ij), products in order of j.
+template <int D>
+__device__ __noinline__ void rotate_dense(float (&v)[2][8], const float *pi_t, int lane) {
+  constexpr int LPR = D / 16;
+  const int j = lane % LPR, first = lane - j;
+  float acc[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+    for (int q = 0; q < LPR; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xv = __shfl_sync(TQ_FULL, v[h][e], first + q);
+        const float *row = pi_t + (h * (D / 2) + 8 * q + e) * D + 8 * j;
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+          for (int e2 = 0; e2 < 8; ++e2) acc[h2][e2] = fmaf(__ldg(row + h2 * (D / 2) + e2), xv, acc[h2][e2]);
+      }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[h][e] = acc[h][e];
+}
+
 // 12 warps: 0-3 and 4-7 the softmax of the two query tiles, 8 the products, 9
 // the copies (10 and 11 fill their warpgroup, which hands its registers on).
 template <int D>
 __global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_constant__ PrefillArgs a) {
   using L = Smem<D>;
-  constexpr int NPL = D / 32, SK = L::SK, SV = L::SV;
+  constexpr int SK = L::SK, SV = L::SV;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ __align__(8) uint64_t kfull[SK], kempty[SK], vfull[SV], vempty[SV], sfull[2], pfull[2], ofull[2], qfull,
       fin;
@@ -563,70 +686,66 @@ __global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_cons
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int x = warp >> 2, lq = warp & 3;
-    // ---- query operands: warp lq of a tile prepares its rows 32 lq .. 32 lq + 31
+    // ---- query operands: warp lq of a tile prepares its rows 32 lq .. 32 lq + 31,
+    // LPR lanes a row, eight coordinates of each half a lane (little code: a block
+    // runs it once)
     {
-      constexpr int QB = D == 128 ? 4 : 8;       // rows in flight
+      constexpr int LPR = D / 16, QR = 32 / LPR;
+      const int j = lane % LPR;
       uint8_t *qimg = sm + L::Q + x * 2 * L::OPER;
-      int tt = 32 * lq / a.G, gh = 32 * lq % a.G;    // token of the tile, head of the group
+      const uint32_t magic = 65535u / a.G + 1u;      // r / G = r magic >> 16 for r, G <= 128
 #pragma unroll 1
-      for (int rb = 32 * lq; rb < 32 * lq + 32; rb += QB) {
-        float v[QB][NPL];
-        int64_t off[QB];
-        int at[QB];
+      for (int rb = 32 * lq; rb < 32 * lq + 32; rb += QR) {
+        const int r = rb + lane / LPR, tt = static_cast<int>((r * magic) >> 16), gh = r - tt * a.G;
+        const int tok = tok0 + x * a.tok_tile + tt, at = pos0 + tok;
+        const bool on = tt < a.tok_tile && tok < sp.n && at >= 0;
+        float v[2][8];
+        load_halves<D>(v, a.q, on ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + gh) * a.sh + 8 * j : -1,
+                       a.dtype, a.q_vec);
+        if (a.rc != nullptr) {
+          float cs[2][8];      // cos, sin
+          const int64_t ro = static_cast<int64_t>(on ? at : 0) * (D / 2) + 8 * j;
+          load_table(cs, a.rc + ro, a.rs + ro, a.rope_vec);
 #pragma unroll
-        for (int z = 0; z < QB; ++z) {
-          const int tok = tok0 + x * a.tok_tile + tt;
-          at[z] = pos0 + tok;
-          const bool on = tt < a.tok_tile && tok < sp.n && at[z] >= 0;
-          off[z] = on ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + gh) * a.sh : -1;
-          if (++gh == a.G) {
-            gh = 0;
-            ++tt;
+          for (int e = 0; e < 8; ++e) {
+            const float p = v[0][e], w = v[1][e];
+            v[0][e] = p * cs[0][e] - w * cs[1][e];
+            v[1][e] = w * cs[0][e] + p * cs[1][e];
           }
         }
-        paged_load_rows<QB, NPL>(v, a.q, off, a.dtype, lane);
-        paged_rope_rows<QB, NPL>(v, a.rc, a.rs, at, off, lane);
         float f = a.scale * 1.4426950408889634f;
         if (a.books.pi != nullptr) {
-          // scratch: d floats of this warp's second-term rows, none of which is
-          // written before its batch has been rotated (the last rows' are taken)
-          float *scr = reinterpret_cast<float *>(qimg + L::OPER + (32 * lq + 32) * 128) - D;
-#pragma unroll
-          for (int z = 0; z < QB; ++z) tq_warp_dense<NPL>(v[z], a.books.pi_t, scr, lane);
+          rotate_dense<D>(v, a.books.pi_t, lane);
         } else {
-#pragma unroll
-          for (int z = 0; z < QB; ++z) {
-            tq_apply_signs<NPL>(v[z], a.books.dneg, lane);
-            tq_warp_wht<NPL, true>(v[z], lane);
-          }
+          rotate_hadamard<D>(v, a.books.dneg, j);
           f *= 1.0f / sqrtf(static_cast<float>(D));
         }
+        float m = 0.f;
 #pragma unroll
-        for (int z = 0; z < QB; ++z) {
-          const int r = rb + z;
-          float m = 0.f;
+        for (int e = 0; e < 8; ++e) {
+          v[0][e] *= f;
+          v[1][e] *= f;
+          m = fmaxf(m, fmaxf(fabsf(v[0][e]), fabsf(v[1][e])));
+        }
 #pragma unroll
-          for (int k = 0; k < NPL; ++k) {
-            v[z][k] *= f;
-            m = fmaxf(m, fabsf(v[z][k]));
-          }
-          m = tq_warp_max(m);
-          // a power of two 2^e taken out where fp16 would lose digits or overflow
-          // (between 2^-100 and 2^100)
-          int e = static_cast<int>(__float_as_uint(m) >> 23) - 126;
-          e = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-100, min(100, e)) : 0;
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(TQ_FULL, m, o));
+        // a power of two 2^e taken out where fp16 would lose digits or overflow
+        // (between 2^-100 and 2^100)
+        int e2 = static_cast<int>(__float_as_uint(m) >> 23) - 126;
+        e2 = m > 0.f && (m < 0.125f || m > 8192.f) ? max(-100, min(100, e2)) : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 #pragma unroll
-          for (int k = 0; k < NPL; ++k) {
-            const int c = coord_place<D>(lane + 32 * k);
-            const float w = v[z][k] * down;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = coord_place<D>(8 * j + e + h * (D / 2));
+            const float w = v[h][e] * down;
             const __half hi = __float2half_rn(w);
             uint8_t *dst = qimg + swz(TQ, r, c >> 3) + (c & 7) * 2;
             *reinterpret_cast<__half *>(dst) = hi;
             *reinterpret_cast<__half *>(dst + L::OPER) = __float2half_rn(w - __half2float(hi));
           }
-          if (lane == 0) frow[x][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        }
+        if (j == 0) frow[x][r] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
       }
       sm100::fence_async_smem();
       __syncwarp();
@@ -926,6 +1045,10 @@ int launch_paged_prefill(const tq_codec *c, const PagedView &p, const void *q, i
   a.chunk = pl.chunk;
   a.po = reinterpret_cast<float *>(a.tiles + pl.tile_space);
   a.pml = reinterpret_cast<float2 *>(a.po + static_cast<size_t>(p.N) * Hq * pl.splits * c->d);
+  const int64_t es = dtype == TQ_BF16 ? 2 : 4;
+  const auto al = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0; };
+  a.q_vec = al(q) && st * es % 16 == 0 && sh * es % 16 == 0;
+  a.rope_vec = al(rc) && al(rs);
   a.wait_outer = 1u << 12;
   if (const char *e = getenv("TQ_WAIT_LIMIT"))
     a.wait_outer = static_cast<uint32_t>((strtoul(e, nullptr, 10) + (1u << 14) - 1) >> 14);

@@ -450,6 +450,31 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(back[0], near[0]) and torch.equal(back[1], near[1])
 
 
+@pytest.mark.parametrize("new,dtype", [(3, "bf16"), (300, "bf16"), (300, "fp32")])
+def test_rows_off_16_byte_boundaries(new, dtype):
+    """Tensors whose rows start on odd elements: the same answers and codes."""
+    d, Hq, Hkv, page = 128, 8, 4, 64
+    ocodec, ncodec = pt.codecs(d, 4, True, 4)
+    batch = pt.Batch([(700, new), (400, new)] * (1 if new < 100 else 2), page)
+    planes = pt.random_pages(ocodec, batch.pool, Hkv, page)
+    b, rope = batch.device(), tl.rope_device(synth.rope_table(batch.max_len, d, 1e4))
+    g = np.random.default_rng(3)
+    whole = dev(g.standard_normal((batch.N, (Hq + 2 * Hkv) * d + 3)), dtype)
+    w = whole.shape[1]
+    odd = lambda at, H: whole.as_strided((batch.N, H, d), (w, d, 1), 1 + at * d)
+    q, k, v = odd(0, Hq), odd(Hq, Hkv), odd(Hq + Hkv, Hkv)
+    out = []
+    for f in (lambda t: t, lambda t: t.contiguous()):
+        cache = pt.upload(planes, ncodec)
+        native.paged_quantize_kv(ncodec, f(k), f(v), cache, b, rope=rope)
+        out.append((tl.download_cache(cache), attend(ncodec, f(q), pt.upload(planes, ncodec), b, Hkv, rope=rope)))
+    for key in ("kcode", "vcode"):
+        assert np.array_equal(out[0][0][key], out[1][0][key]), key
+    for key in ("kscale", "vnorm"):
+        assert np.all(tl.fp16_close(out[0][0][key], out[1][0][key])), key
+    assert torch.equal(out[0][1], out[1][1])
+
+
 # ------------------------------------------------------------------ use
 
 def test_empty_batches_touch_nothing():
