@@ -4,6 +4,12 @@
 //   out_i = y_i cos - y_{i+d/2} sin,  out_{i+d/2} = y_{i+d/2} cos + y_i sin.
 // ("TurboESM ...", section 2.A: the rotation comes before Pi; the norm before
 // the rotation.)
+//
+// HBM-bound: every row is read and written once.  d / 16 lanes hold a row, eight
+// consecutive coordinates of each half a lane, so both elements of a rotation pair and
+// a 16-byte access are in one thread and the mean takes log2(d / 16) shuffles.  A
+// warp takes one token and some of its heads: the token's angles and the weights
+// stay in registers, and the loads of the next heads are in flight together.
 #include "paged.h"
 
 namespace {
@@ -16,55 +22,166 @@ struct NormRopeArgs {
   int64_t yt[2], yh[2];
   int H[2];
   int N;
-  int dtype, w_dtype;
+  int parts;               // warps of a token
+  int w_dtype;
   float eps;
   const int32_t *pos;
   const float *rc, *rs;
   int rope_len;
 };
 
-// One warp per (token, head); coordinate lane + 32 k in register k.
-template <int D>
-__global__ void __launch_bounds__(256) norm_rope_kernel(NormRopeArgs a) {
-  constexpr int NPL = D / 32, HALF = NPL / 2;
-  const int lane = threadIdx.x & 31;
-  const int heads = a.H[0] + a.H[1];
-  const int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (it >= static_cast<int64_t>(a.N) * heads) return;
-  const int64_t t = it / heads;
-  int h = static_cast<int>(it % heads);
-  const int which = h >= a.H[0];
-  if (which) h -= a.H[0];
-  float x[NPL], ss = 0.f;
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <bool BF16, bool VEC>
+struct Oct {   // eight consecutive elements
+  uint32_t u[BF16 ? 4 : 8];
+  __device__ __forceinline__ void load(const void *base, int64_t off) {
+    constexpr int W = BF16 ? 4 : 8;
+    if (VEC) {
+      const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + off * (BF16 ? 2 : 4));
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    x[k] = tq_load_elem(a.x[which], t * a.st[which] + h * a.sh[which] + lane + 32 * k, a.dtype);
-    ss += x[k] * x[k];
-  }
-  const float f = rsqrtf(tq_warp_sum(ss) * (1.0f / D) + a.eps);
+      for (int i = 0; i < W / 4; ++i) {
+        const uint4 v = p[i];
+        u[4 * i] = v.x;
+        u[4 * i + 1] = v.y;
+        u[4 * i + 2] = v.z;
+        u[4 * i + 3] = v.w;
+      }
+    } else if (BF16) {
+      const uint16_t *p = static_cast<const uint16_t *>(base) + off;
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    x[k] *= f;
-    if (a.w[which] != nullptr) x[k] *= tq_load_elem(a.w[which], lane + 32 * k, a.w_dtype);
-  }
-  if (a.rc != nullptr) {
-    const int64_t p = min(max(a.pos[t], 0), a.rope_len - 1);
+      for (int i = 0; i < 4; ++i) u[i] = p[2 * i] | (static_cast<uint32_t>(p[2 * i + 1]) << 16);
+    } else {
 #pragma unroll
-    for (int k = 0; k < HALF; ++k) {
-      const float c = a.rc[p * (D / 2) + lane + 32 * k], s = a.rs[p * (D / 2) + lane + 32 * k];
-      const float u = x[k], v = x[k + HALF];
-      x[k] = u * c - v * s;
-      x[k + HALF] = v * c + u * s;
+      for (int i = 0; i < W; ++i) u[i] = static_cast<const uint32_t *>(base)[off + i];
     }
   }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    const int64_t o = t * a.yt[which] + h * a.yh[which] + lane + 32 * k;
-    if (a.dtype == TQ_BF16)
-      static_cast<__nv_bfloat16 *>(a.y[which])[o] = __float2bfloat16_rn(x[k]);
-    else
-      static_cast<float *>(a.y[which])[o] = x[k];
+    for (int e = 0; e < 8; ++e)
+      v[e] = BF16 ? __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16) : __uint_as_float(u[BF16 ? 0 : e]);
   }
+  __device__ __forceinline__ void put(const float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 4 : 8); ++e) u[e] = BF16 ? bf16_pair(v[(2 * e) & 7], v[(2 * e + 1) & 7]) : __float_as_uint(v[e]);
+  }
+  __device__ __forceinline__ void store(void *base, int64_t off) const {
+    constexpr int W = BF16 ? 4 : 8;
+    if (VEC) {
+      uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + off * (BF16 ? 2 : 4));
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) p[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    } else if (BF16) {
+      uint16_t *p = static_cast<uint16_t *>(base) + off;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[2 * i] = static_cast<uint16_t>(u[i]);
+        p[2 * i + 1] = static_cast<uint16_t>(u[i] >> 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) static_cast<uint32_t *>(base)[off + i] = u[i];
+    }
+  }
+};
+
+template <int D, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int LPR = D / 16, QR = 32 / LPR, U = BF16 ? 4 : 2;     // rows of a warp at once, in flight
+  const int lane = threadIdx.x & 31, j = lane % LPR;
+  const int64_t wi = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t t = wi / a.parts;
+  if (t >= a.N) return;
+  const int part = static_cast<int>(wi % a.parts), heads = a.H[0] + a.H[1];
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+  }
+  if (a.rc != nullptr) {
+    const int64_t p = static_cast<int64_t>(min(max(a.pos[t], 0), a.rope_len - 1)) * (D / 2) + 8 * j;
+    Oct<false, VEC> c, s;
+    c.load(a.rc, p);
+    s.load(a.rs, p);
+    c.get(cs);
+    s.get(sn);
+  }
+  // heads QR part .., QR parts apart; queries first, then keys
+#pragma unroll 1
+  for (int h0 = QR * part + lane / LPR; h0 - lane / LPR < heads; h0 += U * QR * a.parts) {
+    Oct<BF16, VEC> x[U][2];
+    int side[U], h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int hh = h0 + u * QR * a.parts;
+      side[u] = hh >= a.H[0];
+      h[u] = side[u] ? hh - a.H[0] : hh;
+      if (hh < heads) {
+        const int64_t off = t * (side[u] ? a.st[1] : a.st[0]) + h[u] * (side[u] ? a.sh[1] : a.sh[0]) + 8 * j;
+        x[u][0].load(side[u] ? a.x[1] : a.x[0], off);
+        x[u][1].load(side[u] ? a.x[1] : a.x[0], off + D / 2);
+      } else {
+        h[u] = -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[2][8], w[2][8], ss = 0.f;
+      x[u][0].get(v[0]);
+      x[u][1].get(v[1]);
+      const void *wp = side[u] ? a.w[1] : a.w[0];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[q][e] = 1.f;
+      if (wp != nullptr) {
+        if (a.w_dtype == TQ_BF16) {
+          const uint16_t *p = static_cast<const uint16_t *>(wp) + 8 * j;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[q][e] = tq_bf16_to_f32(__ldg(p + q * (D / 2) + e));
+        } else {
+          const float *p = static_cast<const float *>(wp) + 8 * j;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[q][e] = __ldg(p + q * (D / 2) + e);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[0][e], v[0][e], fmaf(v[1][e], v[1][e], ss));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(TQ_FULL, ss, o);
+      const float f = rsqrtf(ss * (1.0f / D) + a.eps);
+      if (h[u] < 0) continue;
+      float o0[8], o1[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = v[0][e] * f * w[0][e], q = v[1][e] * f * w[1][e];
+        o0[e] = p * cs[e] - q * sn[e];
+        o1[e] = q * cs[e] + p * sn[e];
+      }
+      const int64_t off = t * (side[u] ? a.yt[1] : a.yt[0]) + h[u] * (side[u] ? a.yh[1] : a.yh[0]) + 8 * j;
+      Oct<BF16, VEC> r;
+      r.put(o0);
+      r.store(side[u] ? a.y[1] : a.y[0], off);
+      r.put(o1);
+      r.store(side[u] ? a.y[1] : a.y[0], off + D / 2);
+    }
+  }
+}
+
+template <int D, bool BF16>
+void run(const NormRopeArgs &a, bool vec, unsigned grid, cudaStream_t stream) {
+  if (vec)
+    norm_rope_kernel<D, BF16, true><<<grid, 256, 0, stream>>>(a);
+  else
+    norm_rope_kernel<D, BF16, false><<<grid, 256, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -74,8 +191,11 @@ int launch_norm_rope(const tq_heads *q, const tq_heads *k, int dtype, int w_dtyp
                      cudaStream_t stream) {
   NormRopeArgs a = {};
   const tq_heads *hs[2] = {q, k};
+  const int64_t es = dtype == TQ_BF16 ? 2 : 4;
+  const auto al = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  bool vec = al(rc) && al(rs);
   for (int i = 0; i < 2; ++i) {
-    if (hs[i] == nullptr) continue;
+    if (hs[i] == nullptr || hs[i]->heads == 0) continue;
     a.x[i] = hs[i]->x;
     a.y[i] = hs[i]->y;
     a.w[i] = hs[i]->weight;
@@ -84,21 +204,25 @@ int launch_norm_rope(const tq_heads *q, const tq_heads *k, int dtype, int w_dtyp
     a.yt[i] = hs[i]->y_stride_t;
     a.yh[i] = hs[i]->y_stride_h;
     a.H[i] = hs[i]->heads;
+    vec = vec && al(a.x[i]) && al(a.y[i]) && a.st[i] * es % 16 == 0 && a.sh[i] * es % 16 == 0 &&
+          a.yt[i] * es % 16 == 0 && a.yh[i] * es % 16 == 0;
   }
   a.N = N;
-  a.dtype = dtype;
   a.w_dtype = w_dtype;
   a.eps = eps;
   a.pos = pos;
   a.rc = rc;
   a.rs = rs;
   a.rope_len = rope_len;
-  const int64_t rows = static_cast<int64_t>(N) * (a.H[0] + a.H[1]);
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  // one warp a token for many tokens; more, down to one step each, while the SMs
+  // have room for them
+  const int rows = 512 / d, steps = (a.H[0] + a.H[1] + rows - 1) / rows;
+  a.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(steps, 148 * 32 / static_cast<int64_t>(N))));
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(N) * a.parts + 7) / 8);
   if (d == 64)
-    norm_rope_kernel<64><<<grid, 256, 0, stream>>>(a);
+    dtype == TQ_BF16 ? run<64, true>(a, vec, grid, stream) : run<64, false>(a, vec, grid, stream);
   else
-    norm_rope_kernel<128><<<grid, 256, 0, stream>>>(a);
+    dtype == TQ_BF16 ? run<128, true>(a, vec, grid, stream) : run<128, false>(a, vec, grid, stream);
   tq_count_launch(1);
   return tq_check_launch("norm_rope_kernel");
 }
