@@ -10,6 +10,15 @@
 // operands are table entries: both sides keep fp16's 2^-11 at any norm.  Norms,
 // logits, maxima and sums are fp32; query, centroid and weight are rounded to
 // fp16 once each (2^-11 of an element, against 2^-8 of a bf16 answer).
+//
+// Bound by the ALU pipe: about 24 permutes, logic and shift instructions a warp for
+// each token and KV head, at half an instruction a cycle; the bytes would take a
+// quarter of that.  The rest of the design follows from it: sketch bits become fp16
+// operands by one AND for two (their power of two is taken out of the query), codes by
+// byte permutes, value planes are merged into nibbles once per warp in shared memory
+// instead of by each of the four lanes that read a word.  The loop over a group's two
+// halves is kept rolled: a block runs it a few times, and fetching the code of an
+// unrolled body took longer than running it.
 #include <math_constants.h>
 
 #include <cstdlib>
@@ -71,19 +80,16 @@ __device__ __forceinline__ float ex2(float x) {
 // exponent field, then 2^-14, 2^-13, 2^-11, 2^-7, 2.
 __device__ __forceinline__ float bit_value(int x) { return __half2float(__ushort_as_half(1u << x)); }
 
-// Coordinate of thread column t, element `half` (0 / 1 of a register pair) of
-// k-step ks, operand register r (0: first, 1: second): the order in which
-// nibbles() and the sketch-bit masks leave a plane word.
-template <int D>
-__device__ __forceinline__ int code_coord(int t, int ks, int r, int half) {
-  if (D == 128) return 32 * t + 4 * (4 * (ks & 1) + 2 * r + half) + (ks >> 1);
-  return 16 * t + 4 * (2 * r + half) + ks;
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// Exponent e of the power of two above m, within -100 .. 100 (0 for m = 0).
+__device__ __forceinline__ int pow2_above(float m) {
+  return m > 0.f ? max(-100, min(100, static_cast<int>(__float_as_uint(m) >> 23) - 126)) : 0;
 }
-template <int D>
-__device__ __forceinline__ int bit_coord(int t, int ks, int r, int half) {
-  const int x = 2 * ks + r;
-  return D == 128 ? 32 * t + x + 16 * half : 16 * t + x + 8 * half;
-}
+
+// Orders in which plane words leave coordinates as operands, thread column t, k-step
+// ks, operand register r, half of it:
+//   codes   32 t + 4 (4 (ks % 2) + 2 r + half) + ks / 2     (d = 64: 16 t + 4 (2 r + half) + ks)
+//   sketch  32 t + (2 ks + r) + 16 half                     (d = 64: 16 t + (2 ks + r) + 8 half)
 
 // Rows of a (sequence, KV head): row r is new token r / G, head r % G.  Tokens
 // visible to the query tile that starts at row lo.
@@ -92,18 +98,36 @@ __device__ __forceinline__ int tile_visible(const SeqSpan &sp, int G, int lo, in
   return max(0, min(sp.len, sp.len - sp.n + last / G + 1));
 }
 
+// Shared memory of a block before the warps' rings.
+template <int D, int NT>
+struct Fixed {
+  static constexpr int R = 8 * NT, KS = D / 16, QP = D + 8;     // QP: padded query row
+  uint2 bc[KS * NT * 32];           // code operand fragments
+  uint2 bs[KS * NT * 32];           // sketch operand fragments
+  float4 colc[R];                   // column constants
+  __nv_bfloat16 qh[R * QP], ql[R * QP];   // q' in two bf16 terms
+  float2 red[DW * R];               // per warp: largest |q''|, sum of q''
+  float e1[R];                      // 2^exponent of q'
+  uint64_t bars[DW * 8];
+  float sM[2 * DW * R];             // references and sums of the warps
+  float scr[DW * D];                // dense rotations
+};
+
+// Bytes of a 32-token group in a ring: key planes, value nibbles (the planes arrive
+// there and are merged in place), scales.
+constexpr int nib_stride(int d) { return d / 2 + 16; }       // words, padded against bank conflicts
+__host__ __device__ constexpr uint32_t value_room(int d) { return 8 * nib_stride(d) * 4; }
+
 template <int D, bool K4, bool V4, int NT>
 __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(const __grid_constant__ DecArgs a) {
-  constexpr int NPL = D / 32, KS = D / 16, R = 8 * NT, MT = D / 16;
+  constexpr int NPL = D / 32, KS = D / 16, R = 8 * NT, MT = D / 16, VS = nib_stride(D);
+  using Fx = Fixed<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint2 *bc = reinterpret_cast<uint2 *>(smem);                 // [KS][NT][32] code operand
-  uint2 *bs = bc + KS * NT * 32;                               // [KS][NT][32] sketch operand
-  float4 *colc = reinterpret_cast<float4 *>(bs + KS * NT * 32);   // [R] column constants
-  float *q1 = reinterpret_cast<float *>(colc + R);             // [R][D]
-  float *q2 = q1 + R * D;                                      // [256 / D][R][D]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(q2 + 256 * R);   // [DW][8]
-  float *sM = reinterpret_cast<float *>(bars + DW * 8);        // [DW][R], then [DW][R] sums
-  uint8_t *ring = reinterpret_cast<uint8_t *>(sM + 2 * DW * R);
+  Fx &fx = *reinterpret_cast<Fx *>(smem);
+  uint2 *bc = fx.bc, *bs = fx.bs;
+  float4 *colc = fx.colc;
+  float *sM = fx.sM;
+  uint8_t *ring = smem + (sizeof(Fx) + 127) / 128 * 128;
   float *osum = reinterpret_cast<float *>(ring);               // [DW][R][D + 4], once the ring is drained
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -118,158 +142,163 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
   if (split * a.chunk >= g_end && split > 0) return;
 
   const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
-  const uint32_t kb = 32 * planes * (D / 8), vb = nbv * D * 4;
-  const uint32_t stage_bytes = kb + vb + 192;
+  const uint32_t kb = 32 * planes * (D / 8), vb = nbv * D * 4, so = kb + value_room(D);
+  const uint32_t stage_bytes = so + 192;
   uint8_t *mine = ring + static_cast<size_t>(warp) * a.stages * stage_bytes;
-  uint64_t *bar = bars + warp * 8;
-  if (lane == 0)
+  uint64_t *bar = fx.bars + warp * 8;
+  if (lane == 0) {
     for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
-  if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncwarp();
   const int cnt = g_end > g0 ? (g_end - g0 + DW - 1) / DW : 0;   // this warp's groups
   const int P = 1 << a.p.page_shift;
   int pages = -1;          // lane i: page of group i of the current 32
   uint32_t valid = 0u, phase = 0u;
-  auto issue = [&](int i) {
+  auto issue = [&](int i, int st) {
     if ((i & 31) == 0) {
       const int gi = g0 + (i + lane) * DW;
       pages = i + lane < cnt ? paged_page(a.p, s, gi * 32) : -1;
     }
-    const int page = __shfl_sync(TQ_FULL, pages, i & 31), st = i % a.stages;
+    const int page = __shfl_sync(TQ_FULL, pages, i & 31);
     valid = page >= 0 ? valid | (1u << st) : valid & ~(1u << st);
     if (page >= 0 && lane == 0) {
       const int64_t row = (static_cast<int64_t>(page) * a.Hkv + kvh) * P + (((g0 + i * DW) * 32) & (P - 1));
       uint8_t *dst = mine + st * stage_bytes;
-      sm100::mbar_expect_tx(&bar[st], stage_bytes);
+      sm100::mbar_expect_tx(&bar[st], kb + vb + 192);
       sm100::bulk_g2s(dst, a.kcode + row * planes * (D / 8), kb, &bar[st]);
       sm100::bulk_g2s(dst + kb, a.vcode + (row >> 5) * nbv * D, vb, &bar[st]);
-      sm100::bulk_g2s(dst + kb + vb, a.kscale + row * 2, 128, &bar[st]);
-      sm100::bulk_g2s(dst + kb + vb + 128, a.vnorm + row, 64, &bar[st]);
+      sm100::bulk_g2s(dst + so, a.kscale + row * 2, 128, &bar[st]);
+      sm100::bulk_g2s(dst + so + 128, a.vnorm + row, 64, &bar[st]);
     }
   };
   int issued = 0;
-  for (; issued < a.stages && issued < cnt; ++issued) issue(issued);
+#pragma unroll 1
+  for (; issued < a.stages && issued < cnt; ++issued) issue(issued, issued);
 
-  // ---- queries, while the first groups arrive: q' by warps, q'' = S q' by
-  // threads (row tid % D of S, a 1/(256/D) part of its columns)
-  constexpr int PARTS = 256 / D, PW = D / PARTS;
-  uint4 srow[PW / 8];
-  if (a.books.qjl) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.S + (tid % D) * D + (tid / D) * PW);
-#pragma unroll
-    for (int i = 0; i < PW / 8; ++i) srow[i] = src[i];
-  }
-  {
-    // warp w: rows w, w + 8, ..
-    float x[NT][NPL];
-    int64_t off[NT];
-    int at[NT];
-#pragma unroll
-    for (int z = 0; z < NT; ++z) {
-      const int r = warp + DW * z, tok = (lo + r) / a.G;
-      at[z] = sp.len - sp.n + tok;
-      off[z] = r < nrows && at[z] >= 0
-                   ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + (lo + r) % a.G) * a.sh : -1;
-    }
-    paged_load_rows<NT, NPL>(x, a.q, off, a.dtype, lane);
-    paged_rope_rows<NT, NPL>(x, a.rc, a.rs, at, off, lane);
-#pragma unroll
-    for (int z = 0; z < NT; ++z) {
-      const int r = warp + DW * z;
-      if (a.books.pi != nullptr) {
-        tq_warp_dense<NPL>(x[z], a.books.pi_t, q1 + r * D, lane);
-      } else {
-        tq_apply_signs<NPL>(x[z], a.books.dneg, lane);
-        tq_warp_wht<NPL, true>(x[z], lane);
-#pragma unroll
-        for (int k = 0; k < NPL; ++k) x[z][k] *= 1.0f / sqrtf(static_cast<float>(D));
-      }
-#pragma unroll
-      for (int k = 0; k < NPL; ++k) q1[r * D + lane + 32 * k] = x[z][k];
-    }
-  }
-  __syncthreads();
-  if (a.books.qjl) {
-    float acc[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < PW / 8; ++i) {
-      const uint32_t w[4] = {srow[i].x, srow[i].y, srow[i].z, srow[i].w};
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 *qv = reinterpret_cast<const float4 *>(q1 + r * D + (tid / D) * PW + 8 * i);
-        const float4 u = qv[0], v = qv[1];
-        acc[r] = fmaf(__uint_as_float(w[0] << 16), u.x, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[0] & 0xffff0000u), u.y, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[1] << 16), u.z, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[1] & 0xffff0000u), u.w, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[2] << 16), v.x, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[2] & 0xffff0000u), v.y, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[3] << 16), v.z, acc[r]);
-        acc[r] = fmaf(__uint_as_float(w[3] & 0xffff0000u), v.w, acc[r]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) q2[((tid / D) * R + r) * D + tid % D] = acc[r];
-  }
-  __syncthreads();
-  // column constants and power-of-two scales (fp16 operands in [-1, 1])
+  // ---- queries, while the first groups arrive.  q' by warps (rows w, w + 8, ..),
+  // put straight into the code operand and, in two bf16 terms, into the operand of
+  // q'' = S q'
+#pragma unroll 1
   for (int r = warp; r < R; r += DW) {
-    float m1 = 0.f, m2 = 0.f, sum2 = 0.f, z[NPL];
+    float x[1][NPL];
+    const int tok = (lo + r) / a.G, at[1] = {sp.len - sp.n + tok};
+    const int64_t off[1] = {r < nrows && at[0] >= 0 ? static_cast<int64_t>(sp.row0 + tok) * a.st +
+                                                          (kvh * a.G + (lo + r) % a.G) * a.sh
+                                                    : -1};
+    paged_load_rows<1, NPL>(x, a.q, off, a.dtype, lane);
+    paged_rope_rows<1, NPL>(x, a.rc, a.rs, at, off, lane);
+    float f = 1.f;
+    if (a.books.pi != nullptr) {
+      tq_warp_dense<NPL>(x[0], a.books.pi_t, fx.scr + warp * D, lane);
+    } else {
+      tq_apply_signs<NPL>(x[0], a.books.dneg, lane);
+      tq_warp_wht<NPL, true>(x[0], lane);
+      f = 1.0f / sqrtf(static_cast<float>(D));
+    }
+    float m = 0.f;
 #pragma unroll
     for (int k = 0; k < NPL; ++k) {
-      z[k] = 0.f;
-      if (a.books.qjl)
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) z[k] += q2[(p * R + r) * D + lane + 32 * k];
-      m1 = fmaxf(m1, fabsf(q1[r * D + lane + 32 * k]));
-      m2 = fmaxf(m2, fabsf(z[k]));
-      sum2 += z[k];
+      x[0][k] *= f;
+      m = fmaxf(m, fabsf(x[0][k]));
     }
-    m1 = tq_warp_max(m1);
-    m2 = tq_warp_max(m2);
-    sum2 = tq_warp_sum(sum2);
-    // exponents kept inside fp32 for any finite query
-    const int e1 = m1 > 0.f ? max(-120, ilogbf(m1) + 1) : 0, e2 = m2 > 0.f ? max(-100, ilogbf(m2) + 1) : 0;
-    __syncwarp();
+    m = tq_warp_max(m);
+    const int e = pow2_above(m);
+    const float down = pow2(-e);
+    if (lane == 0) fx.e1[r] = pow2(e);
+    __half *dst = reinterpret_cast<__half *>(bc + (r >> 3) * 32 + 4 * (r & 7));
 #pragma unroll
     for (int k = 0; k < NPL; ++k) {
-      q1[r * D + lane + 32 * k] = ldexpf(q1[r * D + lane + 32 * k], -e1);
-      q2[r * D + lane + 32 * k] = ldexpf(z[k], -e2);
-    }
-    if (lane == 0) {
-      const float sl = a.scale * 1.4426950408889634f;
-      const int pos = sp.len - sp.n + (lo + r) / a.G;
-      colc[r] = make_float4(sl * ldexpf(1.f, e1), sl * 2.f * a.qjl_coef * ldexpf(F_SIGN, e2),
-                            sl * a.qjl_coef * sum2, __int_as_float(r < nrows ? pos : -1));
+      const int c = lane + 32 * k;
+      // k-step, register, half, thread column of coordinate c
+      const int el = D == 128 ? (c & 31) >> 2 : (c & 15) >> 2, tt = D == 128 ? c >> 5 : c >> 4;
+      const int ks = D == 128 ? 2 * (c & 3) + (el >> 2) : c & 3;
+      dst[(ks * NT * 32 + tt) * 4 + (el & 3)] = __float2half_rn(x[0][k] * down);
+      const __nv_bfloat16 h = __float2bfloat16_rn(x[0][k]);
+      fx.qh[r * Fx::QP + c] = h;
+      fx.ql[r * Fx::QP + c] = __float2bfloat16_rn(x[0][k] - __bfloat162float(h));
     }
   }
   __syncthreads();
-  for (int e = tid; e < KS * NT * 32; e += DW * 32) {
-    const int l = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT, n = nt * 8 + (l >> 2), tt = l & 3;
-    uint32_t wc[2], wsn[2];
+  // q'': warp w takes rows 16 w .. 16 w + 15 of S (d = 64: the first four warps)
+  float z[NT][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint32_t c[2], b[2];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        c[h] = __half_as_ushort(__float2half_rn(q1[n * D + code_coord<D>(tt, ks, r, h)]));
-        const int x = 2 * ks + r;   // bit 15 is shifted down to bit 0
-        b[h] = __half_as_ushort(__float2half_rn(q2[n * D + bit_coord<D>(tt, ks, r, h)] *
-                                                (1.0f / (F_SIGN * bit_value(x == 15 ? 0 : x)))));
-      }
-      wc[r] = c[0] | (c[1] << 16);
-      wsn[r] = b[0] | (b[1] << 16);
+    for (int e = 0; e < 4; ++e) z[n][e] = 0.f;
+  const bool sk = a.books.qjl && 16 * warp < D;
+  if (sk) {
+    const uint32_t *sr = reinterpret_cast<const uint32_t *>(a.S) + ((16 * warp + g) * D >> 1) + t;
+#pragma unroll 2
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint32_t a0 = sr[8 * ks], a1 = sr[8 * ks + 4 * D], a2 = sr[8 * ks + 4], a3 = sr[8 * ks + 4 * D + 4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const uint32_t *q = reinterpret_cast<const uint32_t *>((term ? fx.ql : fx.qh) + (8 * n + g) * Fx::QP) + 8 * ks + t;
+          asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+              "{%0,%1,%2,%3};"
+              : "+f"(z[n][0]), "+f"(z[n][1]), "+f"(z[n][2]), "+f"(z[n][3])
+              : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(q[0]), "r"(q[4]));
+        }
     }
-    bc[e] = make_uint2(wc[0], wc[1]);
-    bs[e] = make_uint2(wsn[0], wsn[1]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float mx = fmaxf(fabsf(z[n][e]), fabsf(z[n][e + 2])), su = z[n][e] + z[n][e + 2];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+        su += __shfl_xor_sync(TQ_FULL, su, o);
+      }
+      if (g == 0) fx.red[warp * R + 8 * n + 2 * t + e] = make_float2(mx, su);
+    }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2 * NT; ++i) {
+    // column 8 (i / 2) + 2 t + i % 2
+    const int col = 8 * (i >> 1) + 2 * t + (i & 1);
+    float mx = 0.f, su = 0.f;
+#pragma unroll
+    for (int w = 0; w < DW; ++w) {
+      mx = fmaxf(mx, fx.red[w * R + col].x);
+      su += fx.red[w * R + col].y;
+    }
+    const int e = pow2_above(mx);
+    if (sk) {
+      const float down = pow2(-e);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float zv = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) zv = i == 2 * n + b ? z[n][2 * q + b] : zv;
+        const int c = 16 * warp + g + 8 * q;       // coordinate
+        const int y = D == 128 ? c & 31 : c & 15, x = D == 128 ? y & 15 : y & 7, tt = D == 128 ? c >> 5 : c >> 4;
+        // 1 / (F_SIGN times the operand value of bit x); bit 15 is shifted down to bit 0
+        const float up = __uint_as_float(0x7f000000u - __float_as_uint(F_SIGN * bit_value(x & (x == 15 ? 0 : 15))));
+        reinterpret_cast<__half *>(bs + ((x >> 1) * NT + (col >> 3)) * 32 + 4 * (col & 7) + tt)[2 * (x & 1) +
+                                                                                                (D == 128 ? y >> 4 : y >> 3)] =
+            __float2half_rn(zv * down * up);
+      }
+    }
+    if (warp == 0 && g == 0) {
+      const float sl = a.scale * 1.4426950408889634f;
+      const int pos = sp.len - sp.n + (lo + col) / a.G;
+      colc[col] = make_float4(sl * fx.e1[col], sl * 2.f * a.qjl_coef * F_SIGN * pow2(e), sl * a.qjl_coef * su,
+                              __int_as_float(col < nrows ? pos : -1));
+    }
   }
   __syncthreads();
   sm100::pdl_trigger();
 
-  // ---- groups of 32 tokens.  Row `g` of block b (0..3) of the logits is token
-  // 8 b + 4 (g & 1) + g / 2: the order in which the value operand holds tokens.
+  // ---- groups of 32 tokens, 16 (h = 0, 1) at a time.  Row g of block b (b = 0, 1) of
+  // the logits is token 8 (2 h + b) + 4 (g & 1) + g / 2: the order in which the value
+  // operand holds tokens.
   float acc_o[MT][NT][4];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -278,56 +307,95 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc_o[i][n][e] = 0.f;
   float M[NT][2], den[NT][2];
-  int limit_min = 0x7fffffff;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      M[n][e] = -CUDART_INF_F;
+      M[n][e] = -1e30f;
       den[n][e] = 0.f;
     }
-  for (int r = 0; r < R; ++r) limit_min = min(limit_min, r < nrows ? __float_as_int(colc[r].w) : 0x7fffffff);
+  // the smallest position of the tile's rows: its first token's
+  const int limit_min = sp.len - sp.n + lo / a.G;
   const int tok0 = 4 * (g & 1) + (g >> 1);
   bool ok = true;
+  int stg = 0;
+#pragma unroll 1
   for (int i = 0; i < cnt; ++i) {
-    const int stg = i % a.stages;
     if ((valid >> stg) & 1u) {
-      ok = sm100::mbar_wait(&bar[stg], (phase >> stg) & 1u, a.wait_limit);
-      ok = __all_sync(TQ_FULL, ok);
+      ok = __all_sync(TQ_FULL, sm100::mbar_wait(&bar[stg], (phase >> stg) & 1u, a.wait_limit));
       if (!ok) break;
       phase ^= 1u << stg;
-      const uint8_t *base = mine + stg * stage_bytes;
+      uint8_t *base = mine + stg * stage_bytes;
       const int j0 = (g0 + i * DW) * 32;
-      // ---- logits, 16 tokens (blocks 2 h and 2 h + 1) at a time
-      uint32_t pf[4][NT];     // weights as value-side operand registers, by block
-      float lg[2][NT][4];
+      // ---- value planes to nibbles: the words of coordinates NPL lane .. of all
+      // planes become, for both halves h and the four shifts s, pairs of 4-token nibble
+      // runs of two neighbouring coordinates
+      {
+        uint32_t *vw = reinterpret_cast<uint32_t *>(base + kb);
+        uint32_t w[NPL][4];
 #pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (NPL == 4) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (p < nbv) v = *reinterpret_cast<const uint4 *>(vw + p * D + 4 * lane);
+            w[0][p] = v.x;
+            w[1][p] = v.y;
+            w[NPL - 2][p] = v.z;
+            w[NPL - 1][p] = v.w;
+          } else {
+            uint2 v = make_uint2(0u, 0u);
+            if (p < nbv) v = *reinterpret_cast<const uint2 *>(vw + p * D + 2 * lane);
+            w[0][p] = v.x;
+            w[1][p] = v.y;
+          }
+        }
+        __syncwarp();
+        uint32_t nb[NPL][4];
+#pragma unroll
+        for (int c = 0; c < NPL; ++c) nibbles4<V4>(w[c], nb[c]);
+#pragma unroll
+        for (int sft = 0; sft < 4; ++sft)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x7632 : 0x5410;
+            uint32_t *o = vw + (4 * h + sft) * VS + (NPL / 2) * lane;
+            if (NPL == 4)
+              *reinterpret_cast<uint2 *>(o) =
+                  make_uint2(prmt(nb[0][sft], nb[1][sft], sel), prmt(nb[NPL - 2][sft], nb[NPL - 1][sft], sel));
+            else
+              *o = prmt(nb[0][sft], nb[1][sft], sel);
+          }
+        __syncwarp();
+      }
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        // ---- logits
         float s1[NT][4], s2[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s1[n][e] = s2[n][e] = 0.f;
-        uint32_t w[2][4], sg[2];
+        uint32_t nb[2][4], sg[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint32_t *kr = reinterpret_cast<const uint32_t *>(base) + (8 * (2 * h + b) + tok0) * planes * NPL +
                                (D == 128 ? t : t >> 1);
+          uint32_t w[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) w[b][p] = p < mbk ? kr[p * NPL] : 0u;
+          for (int p = 0; p < 4; ++p) w[p] = p < mbk ? kr[p * NPL] : 0u;
           sg[b] = a.books.qjl ? kr[mbk * NPL] : 0u;
           if (D == 64) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) w[b][p] >>= 16 * (t & 1);
+            for (int p = 0; p < 4; ++p) w[p] >>= 16 * (t & 1);
             sg[b] = prmt(sg[b], 0u, t & 1 ? 0x4342 : 0x4140);
           }
-          if (K4) fold_sign(w[b]);
+          nibbles4<K4>(w, nb[b]);
         }
 #pragma unroll
         for (int sft = 0; sft < 4; ++sft) {
           uint32_t oa[4], ob[4];
-          expand8<K4>(nibbles<K4>(w[0], sft), a.lutk, oa);
-          expand8<K4>(nibbles<K4>(w[1], sft), a.lutk, ob);
+          expand8<K4>(nb[0][sft], a.lutk, oa);
+          expand8<K4>(nb[1][sft], a.lutk, ob);
 #pragma unroll
           for (int hf = 0; hf < (D == 128 ? 2 : 1); ++hf) {
             const int ks = D == 128 ? 2 * sft + hf : sft;
@@ -356,111 +424,102 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
             }
           }
         }
-        // ---- logits in units of log2, value norm added
+        // ---- logits in units of log2, value norm added; the largest of each column
+        float lg[NT][4], inv[2], top[NT][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int tk = 8 * (2 * h + b) + tok0;
-          const uint32_t sc = reinterpret_cast<const uint32_t *>(base + kb + vb)[tk];
+          const uint32_t sc = reinterpret_cast<const uint32_t *>(base + so)[tk];
           const float nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
           const float rho = tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
-          const float nv = fmaxf(tq_half_to_f32(reinterpret_cast<const uint16_t *>(base + kb + vb + 128)[tk]),
-                                 5.9604645e-8f);
+          // (a NaN behind the sequence's end becomes the floor)
+          const float nv = fmaxf(tq_half_to_f32(reinterpret_cast<const uint16_t *>(base + so + 128)[tk]), 5.9604645e-8f);
           const float lnv = __log2f(nv);
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[b]) : "f"(nv));
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float4 cc = colc[n * 8 + 2 * t + e];
-              float v = fmaf(nu, fmaf(cc.x, s1[n][2 * b + e], rho * fmaf(cc.y, s2[n][2 * b + e], -cc.z)), lnv);
-              if (j0 + 31 > limit_min) v = j0 + tk <= __float_as_int(cc.w) ? v : -CUDART_INF_F;
-              lg[h][n][2 * b + e] = v;
+              lg[n][2 * b + e] =
+                  fmaf(nu, fmaf(cc.x, s1[n][2 * b + e], rho * fmaf(cc.y, s2[n][2 * b + e], -cc.z)), lnv);
             }
         }
-      }
-      // ---- reference of the weights: moved only when a weight
-      // would exceed 2^8 (fp16 weights are as exact there as at 1)
-      bool grow = false;
+        if (j0 + 31 > limit_min) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) grow |= lg[h][n][e] > M[n][e & 1] + 8.f;
-      if (__any_sync(TQ_FULL, grow)) {
+            for (int e = 0; e < 4; ++e)
+              if (j0 + 8 * (2 * h + (e >> 1)) + tok0 > __float_as_int(colc[n * 8 + 2 * t + (e & 1)].w))
+                lg[n][e] = -CUDART_INF_F;
+        }
+        bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(lg[0][n][e], lg[0][n][e + 2]), fmaxf(lg[1][n][e], lg[1][n][e + 2]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
-            const float mn = fmaxf(M[n][e], mx);
-            const float corr = mn == -CUDART_INF_F ? 1.f : ex2(M[n][e] - mn);
-            M[n][e] = mn;
-            den[n][e] *= corr;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              acc_o[m][n][e] *= corr;
-              acc_o[m][n][e + 2] *= corr;
-            }
+            top[n][e] = fmaxf(lg[n][e], lg[n][e + 2]);
+            grow |= top[n][e] > M[n][e] + 8.f;
           }
-      }
+        // ---- reference of the weights: moved only when a weight would exceed 2^8
+        // (fp16 weights are as exact there as at 1)
+        if (__any_sync(TQ_FULL, grow)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int tk = 8 * (2 * h + b) + tok0;
-          const float nv = fmaxf(tq_half_to_f32(reinterpret_cast<const uint16_t *>(base + kb + vb + 128)[tk]),
-                                 5.9604645e-8f);
-          const float inv = __frcp_rn(nv);
+            for (int e = 0; e < 2; ++e) {
+              float mx = top[n][e];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+              const float mn = fmaxf(M[n][e], mx), corr = ex2(M[n][e] - mn);
+              M[n][e] = mn;
+              den[n][e] *= corr;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                acc_o[m][n][e] *= corr;
+                acc_o[m][n][e + 2] *= corr;
+              }
+            }
+        }
+        uint32_t pf[2][NT];      // weights as operand registers of the values
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float e[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float v = lg[h][n][2 * b + c];
-              e[c] = v == -CUDART_INF_F ? 0.f : ex2(v - M[n][c]);
-              if (v != -CUDART_INF_F) den[n][c] = fmaf(e[c], inv, den[n][c]);
+              e[c] = ex2(lg[n][2 * b + c] - M[n][c]);
+              den[n][c] = fmaf(e[c], inv[b], den[n][c]);
             }
             const __half2 hv = __floats2half2_rn(e[0], e[1]);
-            pf[2 * h + b][n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&hv));
+            pf[b][n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&hv));
           }
-        }
-      // ---- values: four consecutive coordinates of a thread row at a time
+        // ---- values: rows g and g + 8 of m-tile 2 c4 + m are coordinates 32 c4 + 4 g +
+        // 2 m and the next
+        const uint32_t *vn = reinterpret_cast<const uint32_t *>(base + kb) + (4 * h + t) * VS + 2 * g;
 #pragma unroll
-      for (int c4 = 0; c4 < NPL; ++c4) {
-        uint32_t vw[4][4];
+        for (int c4 = 0; c4 < NPL; ++c4) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(vn + 16 * c4);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (p < nbv) v = *reinterpret_cast<const uint4 *>(base + kb + (p * D + 32 * c4 + 4 * g) * 4);
-          vw[0][p] = v.x;
-          vw[1][p] = v.y;
-          vw[2][p] = v.z;
-          vw[3][p] = v.w;
-        }
+          for (int m = 0; m < 2; ++m) {
+            uint32_t o[4];
+            expand8<V4>(m ? v.y : v.x, a.lutv, o);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t oa[4], ob[4];
-          if (V4) {
-            fold_sign(vw[2 * m]);
-            fold_sign(vw[2 * m + 1]);
-          }
-          expand8<V4>(nibbles<V4>(vw[2 * m], t), a.lutv, oa);
-          expand8<V4>(nibbles<V4>(vw[2 * m + 1], t), a.lutv, ob);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816(acc_o[2 * c4 + m][n], oa[0], ob[0], oa[1], ob[1], pf[0][n], pf[1][n]);
-            mma16816(acc_o[2 * c4 + m][n], oa[2], ob[2], oa[3], ob[3], pf[2][n], pf[3][n]);
+            for (int n = 0; n < NT; ++n) mma16816(acc_o[2 * c4 + m][n], o[0], o[2], o[1], o[3], pf[0][n], pf[1][n]);
           }
         }
       }
       __syncwarp();
     }
     if (issued < cnt) {
-      issue(issued);
+      // the merged nibbles were written by threads, the next copy by the copy engine
+      sm100::fence_async_smem();
+      __syncwarp();
+      issue(issued, stg);
       ++issued;
     }
+    stg = stg + 1 == a.stages ? 0 : stg + 1;
   }
   if (!ok) {
     // a copy never arrived: let the others land, and answer NaN
@@ -495,7 +554,7 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
       float mx = sM[col];
 #pragma unroll
       for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + col]);
-      const float f = mx == -CUDART_INF_F ? 0.f : ex2(M[n][e] - mx);
+      const float f = ex2(M[n][e] - mx);
 #pragma unroll
       for (int c4 = 0; c4 < NPL; ++c4)
         *reinterpret_cast<float4 *>(osum + (warp * R + col) * (D + 4) + 32 * c4 + 4 * g) =
@@ -509,7 +568,7 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
     for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + r]);
     float l = 0.f;
 #pragma unroll
-    for (int w = 0; w < DW; ++w) l += sM[(DW + w) * R + r] * (mx == -CUDART_INF_F ? 0.f : ex2(sM[w * R + r] - mx));
+    for (int w = 0; w < DW; ++w) l += sM[(DW + w) * R + r] * ex2(sM[w * R + r] - mx);
     float x[NPL];
 #pragma unroll
     for (int k = 0; k < NPL; ++k) {
@@ -554,7 +613,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
 #pragma unroll 8
   for (int j = 0; j < n; ++j) {
     const float2 m = ml[j];
-    const float f = mx == -CUDART_INF_F ? 0.f : ex2(m.x - mx);
+    const float f = ex2(m.x - mx);
     l = fmaf(m.y, f, l);
 #pragma unroll
     for (int k = 0; k < NPL; ++k) x[k] = fmaf(a.po[(row * a.splits + j) * D + lane + 32 * k], f, x[k]);
@@ -568,8 +627,11 @@ struct DecPlan {
 };
 
 size_t fixed_smem(int d, int NT) {
-  const size_t R = 8 * NT;
-  return 2 * (d / 16) * NT * 32 * 8 + R * 16 + R * d * 4 + 256 * R * 4 + DW * 8 * 8 + 2 * DW * R * 4;
+  const auto of = [&](auto d64, auto d128) { return d == 64 ? d64 : d128; };
+  const size_t n = NT == 1 ? of(sizeof(Fixed<64, 1>), sizeof(Fixed<128, 1>))
+                           : NT == 2 ? of(sizeof(Fixed<64, 2>), sizeof(Fixed<128, 2>))
+                                     : of(sizeof(Fixed<64, 4>), sizeof(Fixed<128, 4>));
+  return (n + 127) / 128 * 128;
 }
 
 // Query rows a tile: 8, 16 or 32.  Blocks: enough for every SM to hold its two
@@ -589,7 +651,7 @@ DecPlan plan(const tq_codec *c, int num_seqs, int max_new, int max_len, int Hq, 
   p.chunk = static_cast<int>((groups + want - 1) / want);
   p.splits = (groups + p.chunk - 1) / p.chunk;
   const int planes = c->mse_bits_k + c->qjl_k;
-  const size_t stage = 32 * planes * (c->d / 8) + c->bits_v * c->d * 4 + 192;
+  const size_t stage = 32 * planes * (c->d / 8) + value_room(c->d) + 192;
   const size_t fixed = fixed_smem(c->d, p.NT);
   const size_t room = (per_sm == 2 ? 113 * 1024 : 226 * 1024) - fixed;
   const size_t merge = static_cast<size_t>(DW) * 8 * p.NT * (c->d + 4) * 4;

@@ -29,6 +29,11 @@ __device__ __forceinline__ uint32_t nibbles(const uint32_t (&w)[4], int s) {
   return n & 0x77777777u;
 }
 
+// All four nibble words of the plane words at once (n[s] = nibbles(w, s)), pairs of
+// planes merged first; with four planes w holds codes, not yet folded.
+template <bool FOUR>
+__device__ __forceinline__ void nibbles4(uint32_t (&w)[4], uint32_t (&n)[4]);
+
 // Four code planes of an odd-symmetric codebook -> magnitude index planes
 // (0 the smallest) and the plane of negative signs.
 __device__ __forceinline__ void fold_sign(uint32_t (&w)[4]) {
@@ -36,6 +41,25 @@ __device__ __forceinline__ void fold_sign(uint32_t (&w)[4]) {
   w[0] ^= w[3];
   w[1] ^= w[3];
   w[2] ^= w[3];
+}
+
+template <bool FOUR>
+__device__ __forceinline__ void nibbles4(uint32_t (&w)[4], uint32_t (&n)[4]) {
+  if (FOUR) fold_sign(w);
+  // two-bit fields of the even and of the odd elements, at even bits
+  const uint32_t e01 = pick(0x55555555u, w[0], w[1] << 1), o01 = pick(0x55555555u, w[0] >> 1, w[1]);
+  uint32_t e23, o23;
+  if (FOUR) {
+    e23 = pick(0x55555555u, w[2], w[3] << 1);
+    o23 = pick(0x55555555u, w[2] >> 1, w[3]);
+  } else {
+    e23 = w[2] & 0x55555555u;
+    o23 = (w[2] >> 1) & 0x55555555u;
+  }
+  n[0] = pick(0x33333333u, e01, e23 << 2);
+  n[2] = pick(0x33333333u, e01 >> 2, e23);
+  n[1] = pick(0x33333333u, o01, o23 << 2);
+  n[3] = pick(0x33333333u, o01 >> 2, o23);
 }
 
 // Eight fp16 table entries of a nibble word as four pairs (0,1) (2,3) (4,5) (6,7).
