@@ -587,15 +587,16 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
   }
 }
 
-// One warp per answer row: the splits' sums joined, rotated back, stored.
+// One block per answer row: the splits' sums joined (a warp every fourth split, a lane
+// D / 32 neighbouring coordinates), rotated back, stored.
 template <int D>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ DecArgs a, int R) {
   constexpr int NPL = D / 32;
-  __shared__ float dsc[4][D];
+  __shared__ __align__(16) float part[4][D];
+  __shared__ float ls[4], scr[D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + warp;
+  const int64_t row = blockIdx.x;
   sm100::pdl_wait();
-  if (row >= static_cast<int64_t>(a.p.N) * a.Hq) return;
   const int tok = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
   const int s = paged_find_seq(a.p, tok, 1, 0);
   const SeqSpan sp = paged_span(a.p, s);
@@ -610,15 +611,37 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   float l = 0.f, x[NPL];
 #pragma unroll
   for (int k = 0; k < NPL; ++k) x[k] = 0.f;
-#pragma unroll 8
-  for (int j = 0; j < n; ++j) {
+  const float *po = a.po + row * a.splits * D + NPL * lane;
+#pragma unroll 5
+  for (int j = warp; j < n; j += 4) {
     const float2 m = ml[j];
+    float v[NPL];
+    if (NPL == 4) {
+      const float4 u = *reinterpret_cast<const float4 *>(po + static_cast<int64_t>(j) * D);
+      v[0] = u.x;
+      v[1] = u.y;
+      v[NPL - 2] = u.z;
+      v[NPL - 1] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(j) * D);
+      v[0] = u.x;
+      v[1] = u.y;
+    }
     const float f = ex2(m.x - mx);
     l = fmaf(m.y, f, l);
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) x[k] = fmaf(a.po[(row * a.splits + j) * D + lane + 32 * k], f, x[k]);
+    for (int k = 0; k < NPL; ++k) x[k] = fmaf(v[k], f, x[k]);
   }
-  paged_store_row<D>(x, l, a.books, dsc[warp], a.out, a.out_dtype, row, lane);
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) part[warp][NPL * lane + k] = x[k];
+  if (lane == 0) ls[warp] = l;
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int k = 0; k < NPL; ++k)
+      x[k] = (part[0][lane + 32 * k] + part[1][lane + 32 * k]) + (part[2][lane + 32 * k] + part[3][lane + 32 * k]);
+    paged_store_row<D>(x, (ls[0] + ls[1]) + (ls[2] + ls[3]), a.books, scr, a.out, a.out_dtype, row, lane);
+  }
 }
 
 struct DecPlan {
@@ -677,7 +700,7 @@ int run_dec(const DecArgs &a, const DecPlan &pl, cudaStream_t stream) {
   tq_count_launch(1);
   if (pl.splits == 1) return tq_check_launch("paged_decode_kernel");
   const int64_t rows = static_cast<int64_t>(a.p.N) * a.Hq;
-  if (tq_launch_pdl(paged_combine_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, a,
+  if (tq_launch_pdl(paged_combine_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, a,
                     8 * NT) != cudaSuccess)
     return tq_check_launch("paged_combine_kernel");
   tq_count_launch(1);
