@@ -313,18 +313,17 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_dequant_tile_kernel(const __g
       sm100::wait_st();
     }
     if (!(ok = group_ok(1 + g, ok))) break;
-    if (gt == 0) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        sm100::mma_f16_ts(tg + D, tg + 8 * k, sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (D * 16), D * 16, 128),
-                          ID, k > 0 ? 1u : 0u);
-      if (!vals && a.books.qjl) {
+    if (wg == 0) {
+      const int terms = !vals && a.books.qjl ? 2 : 1;
+#pragma unroll 1
+      for (int term = 0; term < terms; ++term) {
+        const uint64_t d0 = sm100::smem_desc(sm100::smem_addr(term ? ts : hs), D * 16, 128);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          sm100::mma_f16_ts(tg + D, tg + D / 2 + 8 * k,
-                            sm100::smem_desc(sm100::smem_addr(ts) + k * 2 * (D * 16), D * 16, 128), ID, 1u);
+          sm100::warp_mma_f16_ts(tg + D, tg + term * (D / 2) + 8 * k, d0 + ((k * 2 * D * 16) >> 4), ID,
+                                 term + k > 0 ? 1u : 0u);
       }
-      sm100::mma_commit(&bars[g]);
+      sm100::warp_mma_commit(&bars[g]);
       ++committed;
     }
     ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);

@@ -445,14 +445,16 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
     if (BF16 && w + 1 < w1) fetch(w + 1);
     sm100::fence_async_smem();
     if (!(ok = group_ok(1 + g, ok))) break;
-    if (gt == 0) {
+    if (wg == 0) {
+      const uint64_t dx = sm100::smem_desc(sm100::smem_addr(xs), XS, 128);
+      const uint64_t dh = sm100::smem_desc(sm100::smem_addr(hs), D * 16, 128);
+#pragma unroll 1
+      for (int term = 0; term < 2; ++term)
 #pragma unroll
-      for (int q = 0; q < 2 * D / 16; ++q) {
-        const int term = q / (D / 16), k = q % (D / 16);
-        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * XS, XS, 128),
-                           sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (D * 16), D * 16, 128), ID, q > 0 ? 1u : 0u);
-      }
-      sm100::mma_commit(&bars[g]);
+        for (int k = 0; k < D / 16; ++k)
+          sm100::warp_mma_f16_ss(tg, dx + ((term * XB + k * 2 * XS) >> 4), dh + ((k * 2 * D * 16) >> 4), ID,
+                                 term + k > 0 ? 1u : 0u);
+      sm100::warp_mma_commit(&bars[g]);
       ++committed;
     }
     ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
@@ -542,14 +544,15 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qkey_kernel(const __grid_cons
       sm100::wait_st();
       r2s[g][hf][r] = r2;
       if (!(ok = group_ok(1 + g, ok))) break;
-      if (gt == 0) {
+      if (wg == 0) {
+        const uint64_t dsk = sm100::smem_desc(sm100::smem_addr(ss), D * 16, 128);
+#pragma unroll 1
+        for (int term = 0; term < 2; ++term)
 #pragma unroll
-        for (int q = 0; q < 2 * D / 16; ++q) {
-          const int term = q / (D / 16), k = q % (D / 16);
-          sm100::mma_f16_ts(tg, tg + D + term * (D / 2) + 8 * k,
-                            sm100::smem_desc(sm100::smem_addr(ss) + k * 2 * (D * 16), D * 16, 128), ID, q > 0 ? 1u : 0u);
-        }
-        sm100::mma_commit(&bars[g]);
+          for (int k = 0; k < D / 16; ++k)
+            sm100::warp_mma_f16_ts(tg, tg + D + term * (D / 2) + 8 * k, dsk + ((k * 2 * D * 16) >> 4), ID,
+                                   term + k > 0 ? 1u : 0u);
+        sm100::warp_mma_commit(&bars[g]);
         ++committed;
       }
       ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
@@ -755,15 +758,16 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_qvalue_kernel(const __grid_co
     if (BF16 && w + 1 < w1) fetch(w + 1);
     sm100::fence_async_smem();
     if (!(ok = group_ok(1 + g, ok))) break;
-    if (gt == 0) {
+    if (wg == 0) {
+      const uint64_t dh = sm100::smem_desc(sm100::smem_addr(hs), 128 * 16, 128);
+      const uint64_t dx = sm100::smem_desc(sm100::smem_addr(xs), XS, 128);
+#pragma unroll 1
+      for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-      for (int q = 0; q < TERMS * 8; ++q) {
-        const int term = q / 8, k = q % 8;
-        sm100::mma_bf16_ss(tg, sm100::smem_desc(sm100::smem_addr(hs) + k * 2 * (128 * 16), 128 * 16, 128),
-                           sm100::smem_desc(sm100::smem_addr(xs) + term * XB + k * 2 * XS, XS, 128), ID,
-                           q > 0 ? 1u : 0u);
-      }
-      sm100::mma_commit(&bars[g]);
+        for (int k = 0; k < 8; ++k)
+          sm100::warp_mma_f16_ss(tg, dh + ((k * 2 * 128 * 16) >> 4), dx + ((term * XB + k * 2 * XS) >> 4), ID,
+                                 term + k > 0 ? 1u : 0u);
+      sm100::warp_mma_commit(&bars[g]);
       ++committed;
     }
     ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
