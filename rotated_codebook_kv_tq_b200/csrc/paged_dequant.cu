@@ -242,78 +242,113 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_dequant_tile_kernel(const __g
   uint32_t ph = 0;
   bool ok = true;
   int committed = 0;
-  const int64_t total = a.units * a.Hkv * sides;
-  for (int64_t w = blockIdx.x * 2 + g; w < total; w += 2 * gridDim.x) {
+  // A group's items are consecutive (side, head, unit) triples: the unit and its pages
+  // are looked up when it changes, and the words of the next item are loaded while the
+  // products of this one run.
+  const int64_t total = a.units * a.Hkv * sides, gid = blockIdx.x * 2 + g, ng = 2 * gridDim.x;
+  const int64_t w1 = total * (gid + 1) / ng;
+  int64_t cur_unit = -1;
+  int s = 0, pos0 = 0, tile0 = 0, page = -1;
+  SeqSpan sp = {0, 0, 0};
+  bool live = false, head_rows = false;     // the unit holds a tile; its first one, with tokens before position 0
+  uint32_t raw[NPL / 2][5], rsc = 0u;
+  auto fetch = [&](int64_t w) {
     const bool vals = sides == 2 ? w & 1 : a.v_out != nullptr;
-    const int64_t q = w / sides;
-    const int unit = static_cast<int>(q / a.Hkv), h = static_cast<int>(q % a.Hkv);
-    const int s = paged_find_seq(a.p, unit, TR, 2);
-    const SeqSpan sp = paged_span(a.p, s);
-    const int pos0 = sp.len - sp.n, lt = unit - paged_unit_base(a.p, s, TR, 2);
-    const int tile0 = ((max(pos0, 0) >> 7) + lt) << 7;
+    const int64_t q = w / sides, unit = q / a.Hkv;
+    const int h = static_cast<int>(q % a.Hkv);
+    if (unit != cur_unit) {
+      cur_unit = unit;
+      s = paged_find_seq(a.p, static_cast<int>(unit), TR, 2);
+      sp = paged_span(a.p, s);
+      pos0 = sp.len - sp.n;
+      const int lt = static_cast<int>(unit) - paged_unit_base(a.p, s, TR, 2);
+      tile0 = ((max(pos0, 0) >> 7) + lt) << 7;
+      live = lt >= 0 && sp.n > 0 && tile0 < sp.len;
+      head_rows = lt == 0 && sp.n > 0 && pos0 < 0;
+      const int i = tile0 + r - pos0;
+      const bool any = __any_sync(TQ_FULL, live && i >= 0 && i < sp.n);
+      page = any ? paged_page(a.p, s, tile0 + 32 * lq) : -1;
+    }
+    if (!live || page < 0) return;
+    const int64_t row32 = (static_cast<int64_t>(page) * a.Hkv + h) * P + ((tile0 + 32 * lq) & (P - 1));
+    if (!vals) {
+      const uint32_t *kr = reinterpret_cast<const uint32_t *>(a.kcode + (row32 + lane) * planes * (D / 8)) + hf * (NPL / 2);
+      rsc = reinterpret_cast<const uint32_t *>(a.kscale)[row32 + lane];
+#pragma unroll
+      for (int x = 0; x < NPL / 2; ++x)
+#pragma unroll
+        for (int p = 0; p < 5; ++p) raw[x][p] = p < planes ? kr[p * NPL + x] : 0u;
+    } else {
+      const uint32_t *vg = a.vcode + (row32 >> 5) * nbv * D + hf * (D / 2);
+      rsc = a.vnorm[row32 + lane];
+#pragma unroll
+      for (int x = 0; x < NPL / 2; ++x)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) raw[x][p] = p < nbv ? vg[p * D + 32 * x + lane] : 0u;
+    }
+  };
+  int64_t w = total * gid / ng;
+  if (w < w1) fetch(w);
+#pragma unroll 1
+  for (; w < w1; ++w) {
+    const bool vals = sides == 2 ? w & 1 : a.v_out != nullptr;
+    const int h = static_cast<int>(w / sides % a.Hkv);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(vals ? a.v_out : a.k_out);
-    if (lt < 0) continue;
-    if (lt == 0 && pos0 < 0) {
+    if (head_rows) {
       // new tokens without a position
       for (int64_t e = gt; e < static_cast<int64_t>(min(-pos0, sp.n)) * (D / 8); e += GT)
         *reinterpret_cast<uint4 *>(out + ((sp.row0 + e / (D / 8)) * a.Hkv + h) * D + 8 * (e % (D / 8))) =
             make_uint4(0u, 0u, 0u, 0u);
     }
-    if (sp.n == 0 || tile0 >= sp.len) continue;
-    const int pos = tile0 + r, i = pos - pos0;
+    if (!live) {
+      if (w + 1 < w1) fetch(w + 1);
+      continue;
+    }
+    const int i = tile0 + r - pos0;
     const bool in = i >= 0 && i < sp.n;
-    const bool any = __any_sync(TQ_FULL, in);
-    const int page = any ? paged_page(a.p, s, tile0 + 32 * lq) : -1;
-    const int64_t row32 = (static_cast<int64_t>(page) * a.Hkv + h) * P + ((tile0 + 32 * lq) & (P - 1));
+    uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(sp.row0 + i) * a.Hkv + h) * D + hf * (D / 2));
     float f = 0.f;
     if (page >= 0) {
       uint32_t o[32];
-      if (!vals) {
-        const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row32 + lane];
-        const uint32_t *kr =
-            reinterpret_cast<const uint32_t *>(a.kcode + (row32 + lane) * planes * (D / 8)) + hf * (NPL / 2);
-        if (in) f = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+      if (in) f = tq_half_to_f32(static_cast<uint16_t>(rsc & 0xffffu));
 #pragma unroll
-        for (int x = 0; x < NPL / 2; ++x) {
-          uint32_t pw[4];
+      for (int x = 0; x < NPL / 2; ++x) {
+        uint32_t pw[4];
+        if (vals) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) pw[p] = p < mbk ? kr[p * NPL + x] : 0u;
+          for (int p = 0; p < 4; ++p) {
+            pw[p] = 0u;
+            if (p < nbv) pw[p] = warp_transpose(raw[x][p], lane);
+          }
+          expand32<V4>(pw, a.lutv, o + 16 * x);
+        } else {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) pw[p] = p < mbk ? raw[x][p] : 0u;
           expand32<K4>(pw, a.lutk, o + 16 * x);
         }
+      }
 #pragma unroll
-        for (int c = 0; c < D / 4; c += 8)
-          sm100::tmem_st8(tl + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
-        if (a.books.qjl) {
-          const float rho = in ? tq_half_to_f32(static_cast<uint16_t>(sc >> 16)) : 0.f;
-          const uint32_t one = __half_as_ushort(__float2half_rn(a.qjl_coef * rho)) * 0x00010001u;
-#pragma unroll
-          for (int x = 0; x < NPL / 2; ++x) {
-            const uint32_t sg = ~kr[mbk * NPL + x];
-#pragma unroll
-            for (int b = 0; b < 16; ++b) o[16 * x + b] = ((sg << (15 - b)) & 0x80008000u) ^ one;
-          }
-#pragma unroll
-          for (int c = 0; c < D / 4; c += 8)
-            sm100::tmem_st8(tl + D / 2 + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
-        }
-      } else {
-        const uint32_t *vg = a.vcode + (row32 >> 5) * nbv * D + hf * (D / 2);
-        if (in) f = tq_half_to_f32(a.vnorm[row32 + lane]);
+      for (int c = 0; c < D / 4; c += 8)
+        sm100::tmem_st8(tl + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
+      if (!vals && a.books.qjl) {
+        const float rho = in ? tq_half_to_f32(static_cast<uint16_t>(rsc >> 16)) : 0.f;
+        const uint32_t one = __half_as_ushort(__float2half_rn(a.qjl_coef * rho)) * 0x00010001u;
 #pragma unroll
         for (int x = 0; x < NPL / 2; ++x) {
-          uint32_t pw[4];
+          uint32_t sg = raw[x][4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) pw[p] = p < nbv ? warp_transpose(vg[p * D + 32 * x + lane], lane) : 0u;
-          expand32<V4>(pw, a.lutv, o + 16 * x);
+          for (int p = 0; p < 4; ++p) sg = p == mbk ? raw[x][p] : sg;
+#pragma unroll
+          for (int b = 0; b < 16; ++b) o[16 * x + b] = ((~sg << (15 - b)) & 0x80008000u) ^ one;
         }
 #pragma unroll
         for (int c = 0; c < D / 4; c += 8)
-          sm100::tmem_st8(tl + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
+          sm100::tmem_st8(tl + D / 2 + hf * (D / 4) + c, reinterpret_cast<const uint32_t(&)[8]>(o[c]));
       }
       sm100::wait_st();
     }
-    if (!(ok = group_ok(1 + g, ok))) break;
-    if (wg == 0) {
+    ok = group_ok(1 + g, ok);
+    if (ok && wg == 0) {
       const int terms = !vals && a.books.qjl ? 2 : 1;
 #pragma unroll 1
       for (int term = 0; term < terms; ++term) {
@@ -326,12 +361,13 @@ __global__ void __launch_bounds__(2 * GT, 1) paged_dequant_tile_kernel(const __g
       sm100::warp_mma_commit(&bars[g]);
       ++committed;
     }
-    ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
+    if (w + 1 < w1) fetch(w + 1);
+    // once a wait has run out the group issues nothing more and its rows are NaN
+    if (ok) ok = sm100::mbar_wait(&bars[g], ph, a.wait_limit);
     ph ^= 1;
     sm100::fence_after_sync();
     f *= 1.0f / sqrtf(static_cast<float>(D));
     if (!__all_sync(TQ_FULL, ok)) f = __int_as_float(0x7fc00000);   // a wait ran out: NaN
-    uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(sp.row0 + i) * a.Hkv + h) * D + hf * (D / 2));
 #pragma unroll
     for (int x = 0; x < NPL / 2; ++x) {
       uint32_t v[32];
