@@ -126,14 +126,14 @@ __device__ __forceinline__ int coord_place(int c) {
 }
 
 // Blocks walk the (token tile, KV head, sequence) items; each keeps the sketch
-// matrix as operand fragments in shared memory.
+// matrix as operand fragments in shared memory.  A warp reads the tile's 128 scales
+// itself, so nothing but the value factors goes through shared memory; the pages,
+// scales and key words of the next item are loaded before the values of this one.
 template <int D, bool K4, bool V4>
 __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_constant__ PrefillArgs a) {
-  constexpr int NPL = D / 32, KS = D / 16, NN = D / 8;
+  constexpr int NPL = D / 32, KS = D / 16, NN = D / 8, VI = 4 * D / 256;
   extern __shared__ __align__(16) uint2 sfrag[];   // [KS][NN][32]
-  __shared__ float nuk[TK], mx[8][2];
-  __shared__ __align__(16) __half nuv[TK];         // by place
-  __shared__ int page[4];
+  __shared__ __align__(16) __half nuv[2][TK];      // by place
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   if (a.books.qjl) {
     // k-step ks, register r, half e of thread column t: sketch row 32 t + 2 ks + r +
@@ -151,77 +151,104 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
       sfrag[e] = make_uint2(w[0], w[1]);
     }
   }
+  __syncthreads();
   const int P = 1 << a.p.page_shift, mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
   const int64_t items = static_cast<int64_t>(a.max_tiles) * a.heads * a.p.num_seqs;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int tl = static_cast<int>(item % a.max_tiles), j0 = tl * TK;
-    const int hl = static_cast<int>(item / a.max_tiles % a.heads), h = a.head0 + hl;
-    const int s = static_cast<int>(item / a.max_tiles / a.heads);
-    const SeqSpan sp = paged_span(a.p, s);
-    if (sp.n == 0 || j0 >= sp.len) continue;
-    uint8_t *img = a.tiles + ((static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles + tl) * tile_bytes(D);
-    __syncthreads();   // the last tile's scales have been read
-    if (tid < 4) page[tid] = j0 + 32 * tid < sp.len ? paged_page(a.p, s, j0 + 32 * tid) : -1;
-    __syncthreads();
-    // cache row of token j of the tile
-    auto row_of = [&](int j) {
-      return (static_cast<int64_t>(page[j >> 5]) * a.Hkv + h) * P + ((j0 + j) & (P - 1));
-    };
-    float nk = 0.f, nv = 0.f;
-    const bool there = tid < TK && page[(tid & (TK - 1)) >> 5] >= 0 && j0 + tid < sp.len;
-    if (there) {
-      const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row_of(tid)];
-      nk = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
-      nv = tq_half_to_f32(a.vnorm[row_of(tid)]);
-    }
-    const uint32_t bits = __ballot_sync(TQ_FULL, there);
-    const float wk = tq_warp_max(nk), wv = tq_warp_max(nv);
-    if (lane == 0) {
-      mx[warp][0] = wk;
-      mx[warp][1] = wv;
-      if (warp < 4) reinterpret_cast<TileHeader *>(img)->there[warp] = bits;
-    }
-    __syncthreads();
-    float kmax = 0.f, vmax = 0.f;
+  const int kg = warp >> 1;                        // keys: the warp's 32-token group
+  int s = -1, j0 = 0, h = 0;
+  int64_t item = blockIdx.x;
+  SeqSpan sp = {0, 0, 0};
+  uint8_t *img = nullptr;
+  int pg[4];
+  uint32_t sc[4], vn[4], w0[4], w1[4], sg0, sg1;
+  auto row_of = [&](int pgi, int j) {              // cache row of token j of the tile
+    return (static_cast<int64_t>(pgi) * a.Hkv + h) * P + ((j0 + j) & (P - 1));
+  };
+  auto pick4 = [](const auto (&x)[4], int i) { return i & 2 ? (i & 1 ? x[3] : x[2]) : (i & 1 ? x[1] : x[0]); };
+  // the first item from `item` on that holds tokens: its pages, scales and key words
+  auto load = [&]() {
+#pragma unroll 1
+    for (; item < items; item += gridDim.x) {
+      const int tl = static_cast<int>(item % a.max_tiles), s1 = static_cast<int>(item / a.max_tiles / a.heads);
+      const int hl = static_cast<int>(item / a.max_tiles % a.heads);
+      if (s1 != s) sp = paged_span(a.p, s = s1);
+      j0 = tl * TK;
+      if (sp.n == 0 || j0 >= sp.len) continue;
+      h = a.head0 + hl;
+      img = a.tiles + ((static_cast<int64_t>(hl) * a.p.num_seqs + s) * a.max_tiles + tl) * tile_bytes(D);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      kmax = fmaxf(kmax, mx[w][0]);
-      vmax = fmaxf(vmax, mx[w][1]);
-    }
-    const int ke = kmax > 0.f ? ilogbf(kmax) + 1 : 0, ve = vmax > 0.f ? ilogbf(vmax) + 1 : 0;
-    if (tid < TK) {
-      nuk[tid] = ldexpf(nk, -ke);
-      nuv[(tid & ~31) + 8 * (tid & 3) + ((tid & 31) >> 2)] = __float2half_rn(ldexpf(nv, -ve));
-    }
-    if (tid == 0) {
-      TileHeader *hd = reinterpret_cast<TileHeader *>(img);
-      hd->k_exp = ldexpf(1.f, ke);
-      hd->v_exp = static_cast<float>(ve);
-      hd->v_inv = ldexpf(1.f, -ve);
-      bool all = j0 + TK <= sp.len;
-      for (int i = 0; i < 4; ++i) all = all && page[i] >= 0;
-      hd->all = all;
-    }
-    __syncthreads();
-    // ---- keys: warp w takes places 16 w .. 16 w + 15, rows g and g + 8
-    {
-      const int tk0 = 32 * (warp >> 1) + 4 * g + 2 * (warp & 1), tk1 = tk0 + 1;
-      const bool on = page[warp >> 1] >= 0;
-      const int64_t base = on ? row_of(tk0) : 0;
+      for (int i = 0; i < 4; ++i) pg[i] = j0 + 32 * i < sp.len ? paged_page(a.p, s, j0 + 32 * i) : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = row_of(pg[i] >= 0 ? pg[i] : 0, 32 * i + lane);
+        sc[i] = reinterpret_cast<const uint32_t *>(a.kscale)[row];
+        vn[i] = a.vnorm[row];
+      }
+      const int kp = pick4(pg, kg);
+      const int64_t base = row_of(kp >= 0 ? kp : 0, 32 * kg + 4 * g + 2 * (warp & 1));
       const uint32_t *kr0 = reinterpret_cast<const uint32_t *>(a.kcode + base * planes * (D / 8)) + (D == 128 ? t : t >> 1);
       const uint32_t *kr1 = kr0 + planes * NPL;
-      uint32_t w0[4], w1[4], sg0 = 0u, sg1 = 0u, sc0 = 0u, sc1 = 0u;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        w0[p] = on && p < mbk ? kr0[p * NPL] : 0u;
-        w1[p] = on && p < mbk ? kr1[p * NPL] : 0u;
+        w0[p] = p < mbk ? kr0[p * NPL] : 0u;
+        w1[p] = p < mbk ? kr1[p * NPL] : 0u;
       }
-      if (a.books.qjl && on) {
-        sg0 = kr0[mbk * NPL];
-        sg1 = kr1[mbk * NPL];
-        sc0 = reinterpret_cast<const uint32_t *>(a.kscale)[base];
-        sc1 = reinterpret_cast<const uint32_t *>(a.kscale)[base + 1];
+      sg0 = a.books.qjl ? kr0[mbk * NPL] : 0u;
+      sg1 = a.books.qjl ? kr1[mbk * NPL] : 0u;
+      break;
+    }
+  };
+  load();
+#pragma unroll 1
+  for (int buf = 0; item < items; buf ^= 1) {
+    // ---- value words, used after the keys
+    uint32_t vw[VI][4];
+#pragma unroll
+    for (int x = 0; x < VI; ++x) {
+      const int c = tid % D, gr = tid / D + x * (256 / D), vp = pick4(pg, gr);
+      const uint32_t *w = a.vcode + (row_of(vp >= 0 ? vp : 0, 32 * gr) >> 5) * nbv * D + c;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) vw[x][p] = p < nbv ? w[p * D] : 0u;
+    }
+    // ---- scales; rows past the end may hold anything: their factor is exactly zero
+    float nk[4], nv[4], kmax = 0.f, vmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool there = pg[i] >= 0 && j0 + 32 * i + lane < sp.len;
+      nk[i] = there ? tq_half_to_f32(static_cast<uint16_t>(sc[i] & 0xffffu)) : 0.f;
+      nv[i] = there ? tq_half_to_f32(static_cast<uint16_t>(vn[i])) : 0.f;
+      kmax = fmaxf(kmax, nk[i]);
+      vmax = fmaxf(vmax, nv[i]);
+    }
+    kmax = fminf(tq_warp_max(kmax), 65504.f);
+    vmax = fminf(tq_warp_max(vmax), 65504.f);
+    const int ke = kmax > 0.f ? ilogbf(kmax) + 1 : 0, ve = vmax > 0.f ? ilogbf(vmax) + 1 : 0;   // in -23 .. 16
+    const float kinv = __int_as_float((127 - ke) << 23), vinv = __int_as_float((127 - ve) << 23);
+    if (warp < 4) nuv[buf][32 * warp + 8 * (lane & 3) + (lane >> 2)] = __float2half_rn(pick4(nv, warp) * vinv);
+    if (tid == 0) {
+      TileHeader *hd = reinterpret_cast<TileHeader *>(img);
+      hd->k_exp = __int_as_float((127 + ke) << 23);
+      hd->v_exp = static_cast<float>(ve);
+      hd->v_inv = vinv;
+      bool all = j0 + TK <= sp.len;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int left = sp.len - j0 - 32 * i;
+        all = all && pg[i] >= 0;
+        hd->there[i] = pg[i] < 0 || left <= 0 ? 0u : left < 32 ? (1u << left) - 1u : TQ_FULL;
       }
+      hd->all = all;
+    }
+    // ---- keys: warp w takes places 16 w .. 16 w + 15, rows g and g + 8
+    uint8_t *vimg = img + tile_bytes(D) - oper_bytes(D);
+    {
+      const int l0 = 4 * g + 2 * (warp & 1);
+      const float nkg = pick4(nk, kg) * kinv;
+      const uint32_t scg = pick4(sc, kg);
+      const float n0 = __shfl_sync(TQ_FULL, nkg, l0), n1 = __shfl_sync(TQ_FULL, nkg, l0 + 1);
+      const uint32_t sc0 = __shfl_sync(TQ_FULL, scg, l0), sc1 = __shfl_sync(TQ_FULL, scg, l0 + 1);
+      const float f0 = n0 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc0 >> 16)) : 0.f;
+      const float f1 = n1 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc1 >> 16)) : 0.f;
       if (D == 64) {
         sg0 = prmt(sg0, 0u, t & 1 ? 0x4342 : 0x4140);
         sg1 = prmt(sg1, 0u, t & 1 ? 0x4342 : 0x4140);
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
       for (int n = 0; n < NN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-      if (a.books.qjl && on) {
+      if (a.books.qjl) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const uint32_t a0 = ((sg0 << (15 - 2 * ks)) & 0x80008000u) ^ 0xbf80bf80u;
@@ -253,10 +280,6 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
           }
         }
       }
-      // rows past the end may hold anything: their factor is exactly zero
-      const float n0 = nuk[tk0], n1 = nuk[tk1];
-      const float f0 = n0 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc0 >> 16)) : 0.f;
-      const float f1 = n1 > 0.f ? a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc1 >> 16)) : 0.f;
       if (K4) {
         fold_sign(w0);
         fold_sign(w1);
@@ -264,62 +287,60 @@ __global__ void __launch_bounds__(256, 2) paged_expand_kernel(const __grid_const
       // a thread's coordinates are places 32 t .. (d = 64: 16 t ..) of its rows
       uint8_t *o = img + HDR;
       const int n0r = 16 * warp + g, ch0 = (D / 32) * t;
+      constexpr int PR = D == 128 ? 4 : 2;        // pairs of a shift
+      uint32_t v0[4], v1[4], e0[4], e1[4];        // a 16-byte chunk of either row, its second terms
 #pragma unroll
       for (int sft = 0; sft < 4; ++sft) {
-        uint32_t c0[4], c1[4], e0[4], e1[4];
+        uint32_t c0[4], c1[4], d0[4], d1[4];
         const uint32_t n8 = nibbles<K4>(w0, sft), m8 = nibbles<K4>(w1, sft);
         expand8<K4>(n8, a.lutk, c0);
         expand8<K4>(m8, a.lutk, c1);
-        if (key_lo(D)) {
-          expand8<K4>(n8, a.lutk_lo, e0);
-          expand8<K4>(m8, a.lutk_lo, e1);
-        }
-        constexpr int PR = D == 128 ? 4 : 2;      // pairs of a shift
-        uint32_t v0[PR], v1[PR], l0[PR], l1[PR];
+        expand8<K4>(n8, a.lutk_lo, d0);
+        expand8<K4>(m8, a.lutk_lo, d1);
 #pragma unroll
         for (int i = 0; i < PR; ++i) {
-          const int n = PR * sft + i;
-          float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&c0[i]));
-          float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&c1[i]));
+          const int n = PR * sft + i, at = PR == 4 ? i : 2 * (sft & 1) + i;
+          const float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&c0[i]));
+          const float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&c1[i]));
+          // the centroids' own second terms
+          const float2 y0 = __half22float2(*reinterpret_cast<const __half2 *>(&d0[i]));
+          const float2 y1 = __half22float2(*reinterpret_cast<const __half2 *>(&d1[i]));
+          const float r00 = n0 * fmaf(f0, acc[n][0], x0.x + y0.x), r01 = n0 * fmaf(f0, acc[n][1], x0.y + y0.y);
+          const float r10 = n1 * fmaf(f1, acc[n][2], x1.x + y1.x), r11 = n1 * fmaf(f1, acc[n][3], x1.y + y1.y);
           if (key_lo(D)) {
-            // the centroids' own second terms
-            const float2 y0 = __half22float2(*reinterpret_cast<const __half2 *>(&e0[i]));
-            const float2 y1 = __half22float2(*reinterpret_cast<const __half2 *>(&e1[i]));
-            split_half(n0 * fmaf(f0, acc[n][0], x0.x + y0.x), n0 * fmaf(f0, acc[n][1], x0.y + y0.y), v0[i], l0[i]);
-            split_half(n1 * fmaf(f1, acc[n][2], x1.x + y1.x), n1 * fmaf(f1, acc[n][3], x1.y + y1.y), v1[i], l1[i]);
+            split_half(r00, r01, v0[at], e0[at]);
+            split_half(r10, r11, v1[at], e1[at]);
           } else {
-            v0[i] = pack_half(n0 * fmaf(f0, acc[n][0], x0.x), n0 * fmaf(f0, acc[n][1], x0.y));
-            v1[i] = pack_half(n1 * fmaf(f1, acc[n][2], x1.x), n1 * fmaf(f1, acc[n][3], x1.y));
+            v0[at] = pack_half(r00, r01);
+            v1[at] = pack_half(r10, r11);
           }
         }
-        if (D == 128) {
-          *reinterpret_cast<uint4 *>(o + swz(TK, n0r, ch0 + sft)) = make_uint4(v0[0], v0[1], v0[PR - 2], v0[PR - 1]);
-          *reinterpret_cast<uint4 *>(o + swz(TK, n0r + 8, ch0 + sft)) = make_uint4(v1[0], v1[1], v1[PR - 2], v1[PR - 1]);
-        } else {
-          uint8_t *p = o + swz(TK, n0r, ch0 + (sft >> 1)) + 8 * (sft & 1);
-          uint8_t *q = o + swz(TK, n0r + 8, ch0 + (sft >> 1)) + 8 * (sft & 1);
-          *reinterpret_cast<uint2 *>(p) = make_uint2(v0[0], v0[1]);
-          *reinterpret_cast<uint2 *>(q) = make_uint2(v1[0], v1[1]);
-          *reinterpret_cast<uint2 *>(p + oper_bytes(D)) = make_uint2(l0[0], l0[1]);
-          *reinterpret_cast<uint2 *>(q + oper_bytes(D)) = make_uint2(l1[0], l1[1]);
+        if (PR == 4 || (sft & 1)) {
+          const int ch = ch0 + (PR == 4 ? sft : sft >> 1);
+          uint8_t *p = o + swz(TK, n0r, ch), *q = o + swz(TK, n0r + 8, ch);
+          *reinterpret_cast<uint4 *>(p) = make_uint4(v0[0], v0[1], v0[2], v0[3]);
+          *reinterpret_cast<uint4 *>(q) = make_uint4(v1[0], v1[1], v1[2], v1[3]);
+          if (key_lo(D)) {
+            *reinterpret_cast<uint4 *>(p + oper_bytes(D)) = make_uint4(e0[0], e0[1], e0[2], e0[3]);
+            *reinterpret_cast<uint4 *>(q + oper_bytes(D)) = make_uint4(e1[0], e1[1], e1[2], e1[3]);
+          }
         }
       }
     }
+    // two buffers: whoever writes this one again has passed the next item's barrier
+    __syncthreads();
+    item += gridDim.x;
+    load();
     // ---- values, transposed: (coordinate, 32-token group) a thread
-    for (int it = tid; it < 4 * D; it += 256) {
-      const int c = it % D, gr = it / D;
-      const bool on = page[gr] >= 0;
-      const uint32_t *vw = a.vcode + (on ? (row_of(32 * gr) >> 5) * nbv * D + c : 0);
-      uint32_t w[4];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) w[p] = on && p < nbv ? vw[p * D] : 0u;
-      if (V4) fold_sign(w);
-      uint8_t *vimg = img + tile_bytes(D) - oper_bytes(D);
+    for (int x = 0; x < VI; ++x) {
+      const int c = tid % D, gr = tid / D + x * (256 / D);
+      if (V4) fold_sign(vw[x]);
 #pragma unroll
       for (int sft = 0; sft < 4; ++sft) {
         uint32_t o[4];
-        expand8<V4>(nibbles<V4>(w, sft), a.lutv, o);
-        const uint4 nu = *reinterpret_cast<const uint4 *>(&nuv[32 * gr + 8 * sft]);
+        expand8<V4>(nibbles<V4>(vw[x], sft), a.lutv, o);
+        const uint4 nu = *reinterpret_cast<const uint4 *>(&nuv[buf][32 * gr + 8 * sft]);
         const uint32_t nw[4] = {nu.x, nu.y, nu.z, nu.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
