@@ -525,7 +525,11 @@ int tq_fq_dequantize(const tq_fq_codec *codec, const tq_cache *cache, int which,
  * seq_lens[s] is smaller than the new tokens, the first ones have no position:
  * not written, zeros as the answer.  Packed rows that belong to no sequence,
  * those behind the last one among them, are left as they were.  num_tokens is the row
- * count of the packed tensors (at most 2^24; at most 65535 sequences).
+ * count of the packed tensors (at most 2^24, and at most 2^31 - 1 rows of all
+ * heads together; at most 65535 sequences).
+ * Every wait inside the kernels is bounded; where one gives up, the append
+ * sets bit 31 of its status word (the codes of the call are then unspecified),
+ * and read-back and attention answer NaN for the rows that waited.
  * Supported: d = 64 and 128, every key and value width, with and without the
  * sketch, Walsh-Hadamard and dense rotations.
  * ------------------------------------------------------------------------ */

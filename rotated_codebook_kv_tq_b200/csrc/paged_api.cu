@@ -22,6 +22,8 @@ int paged_view(const char *who, const tq_codec *c, const tq_cache *cache, const 
     return tq_fail(TQ_ERR_INVALID_ARG, w + ": every cache plane is required");
   if (cache->B <= 0 || cache->Hkv <= 0)
     return tq_fail(TQ_ERR_INVALID_ARG, w + ": cache needs B (pages) and Hkv > 0");
+  if (cache->Hkv > 65535 || static_cast<int64_t>(N) * cache->Hkv > INT32_MAX)
+    return tq_fail(TQ_ERR_INVALID_ARG, w + ": at most 65535 KV heads and 2^31 - 1 rows (tokens x KV heads) a call");
   const int64_t P = cache->rows_cap;
   if (P < 32 || (P & (P - 1)) || P > (1 << 20))
     return tq_fail(TQ_ERR_INVALID_ARG, w + ": the page size (rows_cap) must be a power of two, 32 to 2^20");
@@ -49,7 +51,7 @@ int paged_view(const char *who, const tq_codec *c, const tq_cache *cache, const 
   v->table_stride = b->table_stride;
   v->num_seqs = b->num_seqs;
   v->max_pages = b->max_pages;
-  v->max_new = b->max_new;
+  v->max_new = std::min(b->max_new, N);
   v->max_len = b->max_seq_len;
   v->N = N;
   v->num_pages = cache->B;
@@ -148,8 +150,11 @@ int tq_paged_attention_workspace(const tq_codec *c, const tq_paged_batch *batch,
       batch->max_new < 0 || batch->max_seq_len < 0)
     return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention workspace: bad arguments");
   if (c->d > 128) return tq_fail(TQ_ERR_UNSUPPORTED, "paged_attention workspace: d must be 64 or 128");
-  *bytes = paged_attn_workspace_bytes(c, num_tokens, batch->num_seqs, batch->max_new, batch->max_seq_len, Hq,
-                                      Hkv);
+  if (num_tokens > (1 << 24) || Hq > 65535 || static_cast<int64_t>(num_tokens) * Hq > INT32_MAX ||
+      batch->num_seqs > 65535 || batch->max_seq_len > (1 << 30))
+    return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention workspace: beyond the limits of a call");
+  *bytes = paged_attn_workspace_bytes(c, num_tokens, batch->num_seqs, std::min(batch->max_new, num_tokens),
+                                      batch->max_seq_len, Hq, Hkv);
   return TQ_OK;
 }
 
@@ -162,6 +167,8 @@ int tq_paged_attention(const tq_codec *c, const void *q, int dtype, int num_toke
   if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention: dtype");
   if (Hq <= 0 || Hq % cache->Hkv || Hq > 65535)
     return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention: Hq must be a multiple of Hkv, at most 65535");
+  if (static_cast<int64_t>(num_tokens) * Hq > INT32_MAX)
+    return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention: at most 2^31 - 1 rows (tokens x query heads) a call");
   if (!std::isfinite(scale)) return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention: scale not finite");
   if (int e = check_rope("paged_attention", rope_cos, rope_sin, rope_len, view.max_len)) return e;
   if (empty(view)) return TQ_OK;

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
   float *osum = reinterpret_cast<float *>(ring);               // [DW][R][D + 4], once the ring is drained
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, kvh = blockIdx.y / a.qtiles, qt = blockIdx.y % a.qtiles, s = blockIdx.z;
+  const int split = blockIdx.x % a.splits, qt = blockIdx.x / a.splits, kvh = blockIdx.y, s = blockIdx.z;
   sm100::pdl_wait();
   const SeqSpan sp = paged_span(a.p, s);
   const int lo = qt * R, nrows = min(R, sp.n * a.G - lo);
@@ -518,6 +518,8 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
       __syncwarp();
       issue(issued, stg);
       ++issued;
+    } else {
+      valid &= ~(1u << stg);      // nothing of this slot is awaited any more
     }
     stg = stg + 1 == a.stages ? 0 : stg + 1;
   }
@@ -694,7 +696,7 @@ int run_dec(const DecArgs &a, const DecPlan &pl, cudaStream_t stream) {
       return tq_check_launch("cudaFuncSetAttribute(paged_decode)");
     done[dev] = true;
   }
-  const dim3 grid(pl.splits, a.Hkv * pl.qtiles, a.p.num_seqs);
+  const dim3 grid(pl.splits * pl.qtiles, a.Hkv, a.p.num_seqs);
   if (tq_launch_pdl(kern, grid, dim3(DW * 32), pl.smem, stream, a) != cudaSuccess)
     return tq_check_launch("paged_decode_kernel");
   tq_count_launch(1);

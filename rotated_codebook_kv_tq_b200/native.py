@@ -634,32 +634,22 @@ def fq_dequantize(codec: FqCodec, cache: Cache, which: int, row0: int, rows: int
 
 # ---------------------------------------------------------------- paged cache
 
-@dataclass
+@dataclass(frozen=True)
 class PagedBatch:
     """A ``tq_paged_batch``: the new tokens of several sequences over a paged
     cache (an ``alloc_cache`` whose batch is the page pool and whose rows_cap is
     the page size).  page_table int32 [S, max_pages], q_start int32 [S + 1],
-    seq_lens int32 [S] are device tensors, read when the kernels run; max_new
-    and max_seq_len are their host-side limits."""
+    seq_lens int32 [S] are device tensors, read when the kernels run (their
+    contents may change between calls); max_new and max_seq_len are their
+    host-side limits."""
     page_table: "object"
     q_start: "object"
     seq_lens: "object"
     max_new: int
     max_seq_len: int
 
-    def desc(self) -> PagedBatchDesc:
-        t = self.page_table
-        key = (t.data_ptr(), self.q_start.data_ptr(), self.seq_lens.data_ptr(), t.stride(0),
-               self.seq_lens.shape[0], t.shape[1], self.max_new, self.max_seq_len)
-        cached = self.__dict__.get("_desc")
-        if cached is None or cached[0] != key:
-            self._check()
-            cached = (key, PagedBatchDesc(*key))
-            self.__dict__["_desc"] = cached
-        return cached[1]
-
-    def _check(self) -> None:
-        import torch
+    def __post_init__(self) -> None:
+        torch = _torch()
         t, S = self.page_table, self.seq_lens.shape[0]
         if any(x.dtype != torch.int32 for x in (t, self.q_start, self.seq_lens)):
             raise TypeError("page_table, q_start and seq_lens must be int32")
@@ -669,36 +659,64 @@ class PagedBatch:
                                                          self.seq_lens.is_contiguous()):
             raise ValueError("page_table rows, q_start and seq_lens must be contiguous")
 
+    def desc(self) -> PagedBatchDesc:
+        t = self.page_table
+        return PagedBatchDesc(t.data_ptr(), self.q_start.data_ptr(), self.seq_lens.data_ptr(), t.stride(0),
+                              t.shape[0], t.shape[1], self.max_new, self.max_seq_len)
+
+
+_TORCH = None
+
+
+def _torch():
+    """torch, without an import statement in every call."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _on_current_device(tensors) -> None:
+    """The kernels run on the current device: a tensor elsewhere is refused."""
+    cuda = _torch().cuda
+    here = cuda.current_device() if cuda.is_initialized() else -1
+    for t in tensors:
+        if t is not None and t.get_device() != here or here < 0:
+            raise ValueError("every tensor must be on the current CUDA device")
+
 
 def _packed(name: str, t, d: int):
-    """Strides (token, head) of a packed [N, H, d] tensor with d contiguous."""
-    if t.dim() != 3 or t.shape[2] != d or t.stride(2) != 1:
+    """Shape and strides of a packed [N, H, d] tensor with d contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != d or stride[2] != 1:
         raise ValueError(f"{name} must be [tokens, heads, {d}] with the last dim contiguous")
-    return t.stride(0), t.stride(1)
+    return shape, stride
 
 
 def _rope_args(rope, d: int):
     if rope is None:
         return None, None, 0
     c, s = rope
-    if c.shape != s.shape or c.dim() != 2 or c.shape[1] != d // 2 or not (c.is_contiguous() and s.is_contiguous()) \
-            or _dtype_code(c) != TQ_F32 or _dtype_code(s) != TQ_F32:
+    shape, f32 = c.shape, _torch().float32
+    if (s.shape != shape or len(shape) != 2 or 2 * shape[1] != d or c.dtype is not f32 or s.dtype is not f32
+            or not (c.is_contiguous() and s.is_contiguous())):
         raise ValueError(f"rope must be two contiguous fp32 tables [positions, {d // 2}]")
-    return c.data_ptr(), s.data_ptr(), c.shape[0]
+    return c.data_ptr(), s.data_ptr(), shape[0]
 
 
 def paged_quantize_kv(codec: Codec, k, v, cache: Cache, batch: PagedBatch, rope=None, status=None,
                       stream=None) -> None:
     """tq_paged_quantize_kv: the new tokens' k, v [N, Hkv, d] (same strides)
     coded into their pages, keys rotated at their positions first."""
-    N, H, d = k.shape
-    st, sh = _packed("k", k, codec.d)
-    if v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype or H != cache.Hkv:
+    shape, stride = _packed("k", k, codec.d)
+    dtype = k.dtype
+    if v.shape != shape or v.stride() != stride or v.dtype != dtype or shape[1] != cache.Hkv:
         raise ValueError("k and v need the same shape, strides and dtype, and the cache's KV heads")
     rc, rs, rn = _rope_args(rope, codec.d)
-    check(lib().tq_paged_quantize_kv(codec.handle, k.data_ptr(), v.data_ptr(), _dtype_code(k), N, st, sh,
-                                     rc, rs, rn, ctypes.byref(cache.desc()), ctypes.byref(batch.desc()),
-                                     _ptr(status), _stream(stream)))
+    _on_current_device((k, v, status, batch.seq_lens) + (rope or ()))
+    check(lib().tq_paged_quantize_kv(codec.handle, k.data_ptr(), v.data_ptr(), _code_of(dtype), shape[0], stride[0],
+                                     stride[1], rc, rs, rn, cache.desc(), batch.desc(), _ptr(status), _stream(stream)))
 
 
 def paged_dequantize(codec: Codec, cache: Cache, batch: PagedBatch, k_out, v_out, stream=None) -> None:
@@ -707,19 +725,18 @@ def paged_dequantize(codec: Codec, cache: Cache, batch: PagedBatch, k_out, v_out
     ref = k_out if k_out is not None else v_out
     if ref is None:
         raise ValueError("k_out or v_out is required")
+    N, dtype = ref.shape[0], ref.dtype
     for t in (k_out, v_out):
-        if t is not None and (tuple(t.shape) != (ref.shape[0], cache.Hkv, codec.d) or t.dtype != ref.dtype
-                              or not t.is_contiguous()):
+        if t is not None and (t.shape != (N, cache.Hkv, codec.d) or t.dtype != dtype or not t.is_contiguous()):
             raise ValueError(f"outputs must be contiguous [tokens, {cache.Hkv}, {codec.d}] of one dtype")
-    check(lib().tq_paged_dequantize(codec.handle, ctypes.byref(cache.desc()), ctypes.byref(batch.desc()),
-                                    ref.shape[0], _ptr(k_out), _ptr(v_out), _dtype_code(ref),
-                                    _stream(stream)))
+    _on_current_device((k_out, v_out, batch.seq_lens))
+    check(lib().tq_paged_dequantize(codec.handle, cache.desc(), batch.desc(), N, _ptr(k_out), _ptr(v_out),
+                                    _code_of(dtype), _stream(stream)))
 
 
 def paged_attention_workspace(codec: Codec, batch: PagedBatch, num_tokens: int, Hq: int, Hkv: int) -> int:
     n = ctypes.c_size_t(0)
-    check(lib().tq_paged_attention_workspace(codec.handle, ctypes.byref(batch.desc()), num_tokens, Hq, Hkv,
-                                             ctypes.byref(n)))
+    check(lib().tq_paged_attention_workspace(codec.handle, batch.desc(), num_tokens, Hq, Hkv, ctypes.byref(n)))
     return n.value
 
 
@@ -727,28 +744,27 @@ def paged_attention(codec: Codec, q, cache: Cache, batch: PagedBatch, scale: flo
                     rope=None, stream=None) -> None:
     """tq_paged_attention: q [N, Hq, d] of the new tokens, each over the cached
     tokens up to its own position -> out [N, Hq, d] (fp32 or bf16)."""
-    N, Hq, d = q.shape
-    st, sh = _packed("q", q, codec.d)
-    if out.shape != q.shape or not out.is_contiguous():
+    shape, stride = _packed("q", q, codec.d)
+    if out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be contiguous and shaped like q")
     rc, rs, rn = _rope_args(rope, codec.d)
-    check(lib().tq_paged_attention(codec.handle, q.data_ptr(), _dtype_code(q), N, Hq, st, sh,
-                                   ctypes.byref(cache.desc()), ctypes.byref(batch.desc()), float(scale),
-                                   rc, rs, rn, workspace.data_ptr(),
+    _on_current_device((q, out, workspace, batch.seq_lens) + (rope or ()))
+    check(lib().tq_paged_attention(codec.handle, q.data_ptr(), _code_of(q.dtype), shape[0], shape[1], stride[0],
+                                   stride[1], cache.desc(), batch.desc(), scale, rc, rs, rn, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), out.data_ptr(),
-                                   _dtype_code(out), _stream(stream)))
+                                   _code_of(out.dtype), _stream(stream)))
 
 
-def _heads(name: str, x, y, w, d: int) -> Optional[HeadsDesc]:
-    if x is None:
-        return None
-    st, sh = _packed(name, x, d)
-    if y is None or y.shape != x.shape or y.dtype != x.dtype:
+def _heads(name: str, x, y, w, d: int) -> HeadsDesc:
+    shape, xs = _packed(name, x, d)
+    if y is None or y.shape != shape or y.dtype != x.dtype:
         raise ValueError(f"{name}: the output must have the input's shape and dtype")
-    yt, yh = _packed(name, y, d)
+    ys = y.stride()
+    if ys[2] != 1:
+        raise ValueError(f"{name}: the output's last dim must be contiguous")
     if w is not None and (w.shape != (d,) or not w.is_contiguous()):
         raise ValueError(f"{name}: the weight must be [{d}]")
-    return HeadsDesc(x.data_ptr(), y.data_ptr(), _ptr(w), st, sh, yt, yh, x.shape[1])
+    return HeadsDesc(x.data_ptr(), y.data_ptr(), _ptr(w), xs[0], xs[1], ys[0], ys[1], shape[1])
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, q_out, k_out, rope=None,
@@ -760,25 +776,21 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, q_out, k_out, 
     if ref is None:
         raise ValueError("q or k is required")
     N, _, d = ref.shape
-    if q is not None and k is not None and (k.shape[0] != N or k.shape[2] != d or k.dtype != q.dtype):
+    dtype = ref.dtype
+    if q is not None and k is not None and (k.shape[0] != N or k.dtype != dtype):
         raise ValueError("q and k need the same tokens, head dim and dtype")
     w = q_weight if q_weight is not None else k_weight
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise ValueError("q_weight and k_weight need the same dtype")
     rc, rs, rn = _rope_args(rope, d)
-    if positions is not None and (_is_int32(positions) is False or positions.shape != (N,)
+    if positions is not None and (positions.dtype is not _torch().int32 or positions.shape != (N,)
                                   or not positions.is_contiguous()):
         raise ValueError("positions must be contiguous int32 [tokens]")
-    dq, dk = _heads("q", q, q_out, q_weight, d), _heads("k", k, k_out, k_weight, d)
-    check(lib().tq_qk_norm_rope(None if dq is None else ctypes.byref(dq),
-                                None if dk is None else ctypes.byref(dk), _dtype_code(ref),
-                                TQ_F32 if w is None else _dtype_code(w), d, N, float(eps), _ptr(positions),
-                                rc, rs, rn, _stream(stream)))
-
-
-def _is_int32(t) -> bool:
-    import torch
-    return t.dtype == torch.int32
+    dq = None if q is None else _heads("q", q, q_out, q_weight, d)
+    dk = None if k is None else _heads("k", k, k_out, k_weight, d)
+    code, w_code = _code_of(dtype), TQ_F32 if w is None else _code_of(w.dtype)
+    _on_current_device((q, k, q_weight, k_weight, positions, q_out, k_out) + (rope or ()))
+    check(lib().tq_qk_norm_rope(dq, dk, code, w_code, d, N, eps, _ptr(positions), rc, rs, rn, _stream(stream)))
 
 
 def set_timing_events(start=None, stop=None) -> None:

@@ -189,3 +189,34 @@ def test_binding_refusals():
         native.qk_norm_rope(x.transpose(1, 2), None, None, None, 1e-6, None, x, None)
     with pytest.raises(TypeError):
         native.qk_norm_rope(x.half(), None, None, None, 1e-6, None, x.half(), None)
+
+
+def test_row_limits_of_a_call(L, codec):
+    """Row counts that no launch could cover are refused, not cut off."""
+    c, n = codec[64], ctypes.c_size_t(0)
+    many = dict(N=1 << 24, ca=cache(heads=256))
+    assert quantize(L, c, **many) == native.TQ_ERR_INVALID_ARG
+    assert dequantize(L, c, **many) == native.TQ_ERR_INVALID_ARG
+    assert attention(L, c, Hq=256, **many) == native.TQ_ERR_INVALID_ARG
+    assert attention(L, c, N=1 << 24, Hq=256, ca=cache(heads=1)) == native.TQ_ERR_INVALID_ARG
+    assert quantize(L, c, ca=cache(heads=65536)) == native.TQ_ERR_INVALID_ARG
+    for N, Hq in ((1 << 24, 256), ((1 << 24) + 1, 4), (8, 65536 * 2)):
+        assert L.tq_paged_attention_workspace(c, ctypes.byref(batch()), N, Hq, 1,
+                                              ctypes.byref(n)) == native.TQ_ERR_INVALID_ARG
+    # a limit on new tokens far above the call's tokens counts as the call's
+    for Hq in (8, 160):
+        sizes = []
+        for most in (8, (1 << 31) - 1):
+            assert L.tq_paged_attention_workspace(c, ctypes.byref(batch(max_new=most)), 8, Hq, 1,
+                                                  ctypes.byref(n)) == native.TQ_OK
+            sizes.append(n.value)
+        assert sizes[0] == sizes[1]
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("covered there with a device")
+    x = torch.zeros((2, 3, 64))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        native.qk_norm_rope(x, None, None, None, 1e-6, None, x, None)
