@@ -582,6 +582,8 @@ int tq_paged_dequantize(const tq_codec *codec, const tq_cache *cache, const tq_p
  * workspace device, >= tq_paged_attention_workspace(...) bytes for the same
  *           batch limits, 16-byte aligned; needs no initialisation.  Calls
  *           that may run at the same time need workspaces of their own.
+ * Calls of few rows (num_tokens x Hq, counted in tiles of 8 to 32 rows, times
+ * max_seq_len / 256) beyond 2^31 are refused.
  * Products run on the tensor cores from fp16 and bf16 operands with fp32
  * sums: about 2e-3 of the output's norm for logits of a few tens. */
 int tq_paged_attention_workspace(const tq_codec *codec, const tq_paged_batch *batch,

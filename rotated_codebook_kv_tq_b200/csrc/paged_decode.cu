@@ -1,7 +1,8 @@
-// Attention of a few new tokens over a paged compressed cache: the keys of a
-// (sequence, KV head) are split over blocks, expanded from their code planes
-// straight into tensor-core operand registers, and the blocks' partial sums
-// joined by a second kernel.
+// Attention of a few new tokens over a paged compressed cache: the 32-token groups
+// of all (sequence, KV head, query tile) pairs in one row are cut into equal ranges, one
+// a resident block; codes are expanded from their planes straight into tensor-core
+// operand registers, and the sums of a pair that lies in several blocks joined by a
+// second kernel.
 //
 //   l_ij = scale nu_j (<q'_i, c[idx_j]> + coef rho_j (2 <q''_i, sigma_j> - sum q''_i)),
 //   q' = Pi RoPE(q), q'' = S q', coef = sqrt(pi/2)/d, sigma_j the 0/1 sketch bits;
@@ -46,12 +47,12 @@ struct DecArgs {
   void *out;
   int out_dtype;
   const uint16_t *S;
-  int qtiles;            // tiles of 8 NT query rows a (sequence, KV head)
-  int chunk;             // 32-token groups of a block
-  int splits;
+  int blocks;
+  int scan;              // sequences a lane sums up
   int stages;            // ring slots of a warp
-  float *po;             // [N Hq][splits][D] partial sums
-  float2 *pml;           // [N Hq][splits] (reference M, denominator)
+  float *po;             // [blocks][2][rows of a tile][D] partial sums
+  float2 *pml;           // [blocks][2][rows of a tile] (reference M, denominator)
+  int2 *info;            // [N Hq] (slot of the first part, parts)
   uint32_t wait_limit;
   uint32_t lutk[4], lutv[4];   // fp16 table bytes: low 0-3, low 4-7, high 0-3, high 4-7
   TqBooks books;
@@ -98,6 +99,23 @@ __device__ __forceinline__ int tile_visible(const SeqSpan &sp, int G, int lo, in
   return max(0, min(sp.len, sp.len - sp.n + last / G + 1));
 }
 
+// A pair's share of a block.
+struct Segment {
+  SeqSpan sp;
+  int s, kvh, lo;          // sequence, KV head, first query row
+  int g_begin, g_end;      // 32-token groups
+  uint32_t rounds;
+  int parts, part;         // of the pair, and which one this is
+  int slot, slot0;         // of this part's sums, and of part 0's
+};
+
+// How the work is cut.  It is counted in rounds: a group for each of a block's warps.  A
+// block's range is `per` rounds; a pair takes a multiple of `unit`: 1, so that the ranges
+// are even, or `per`, so that no block has two pairs.
+struct Cut {
+  uint32_t per, unit, pos, end;     // this block's range: what is left of it
+};
+
 // Shared memory of a block before the warps' rings.
 template <int D, int NT>
 struct Fixed {
@@ -111,7 +129,121 @@ struct Fixed {
   uint64_t bars[DW * 8];
   float sM[2 * DW * R];             // references and sums of the warps
   float scr[DW * D];                // dense rotations
+  Cut cut;
+  uint32_t before[32];              // rounds of the sequences before a lane's
+  Segment seg;
 };
+
+__device__ __forceinline__ uint32_t up_to(uint32_t n, uint32_t unit) { return (n + unit - 1) / unit * unit; }
+__device__ __forceinline__ uint32_t seq_rounds(const SeqSpan &sp) { return max(1, (sp.len + 32 * DW - 1) / (32 * DW)); }
+template <int R>
+__device__ __forceinline__ uint32_t seq_pairs(const DecArgs &a, const SeqSpan &sp) {
+  return static_cast<uint32_t>(a.Hkv) * ((sp.n * a.G + R - 1) / R);
+}
+
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(TQ_FULL, v, o);
+    v += lane >= o ? u : 0u;
+  }
+  return v;
+}
+
+// The cut and the running sums of the sequences' rounds, by a warp.  A second pair costs
+// a block about as much as two rounds (its queries, the ring's start and end), so ranges
+// that hold one pair only are taken where they are at most that much longer.
+template <int R, typename Fx>
+__device__ __forceinline__ void cut_work(const DecArgs &a, Fx &fx, int lane) {
+  const int s0 = lane * a.scan, s1 = min(s0 + a.scan, a.p.num_seqs);
+  uint32_t n = 0u, r = 0u;      // pairs of the lane's last sequence, their rounds
+  const auto load = [&](int s) {
+    const SeqSpan sp = paged_span(a.p, s);
+    n = seq_pairs<R>(a, sp);
+    r = seq_rounds(sp);
+  };
+  uint32_t pairs = 0u, rounds = 0u;
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    load(s);
+    pairs += n;
+    rounds += n * r;
+  }
+  uint32_t total = __reduce_add_sync(TQ_FULL, rounds);
+  uint32_t per = (total + a.blocks - 1) / a.blocks, unit = 1u;
+  if (total > 0u && __reduce_add_sync(TQ_FULL, pairs) <= a.blocks) {
+#pragma unroll 1
+    for (uint32_t p = per; p < per + 3; ++p) {
+      uint32_t padded = n * up_to(r, p);
+      for (int s = s0; s < s1 && a.scan > 1; ++s) {
+        if (s == s0) padded = 0u;
+        load(s);
+        padded += n * up_to(r, p);
+      }
+      const uint32_t all = __reduce_add_sync(TQ_FULL, padded);
+      if (all <= a.blocks * p) {
+        per = unit = p;
+        rounds = padded;
+        total = all;
+        break;
+      }
+    }
+  }
+  fx.before[lane] = warp_scan(rounds, lane) - rounds;
+  if (lane == 0) fx.cut = {per, unit, blockIdx.x * per, min((blockIdx.x + 1) * per, total)};
+  __syncwarp();
+}
+
+// The next segment of the block's range, by a warp; rounds = 0 at its end.
+template <int R, typename Fx>
+__device__ __forceinline__ void next_segment(const DecArgs &a, Fx &fx, int lane) {
+  const Cut c = fx.cut;
+  Segment &g = fx.seg;
+  if (c.pos >= c.end) {
+    if (lane == 0) g.rounds = 0u;
+    return;
+  }
+  const int i = __popc(__ballot_sync(TQ_FULL, fx.before[lane] <= c.pos)) - 1;    // the lane whose sequences hold pos
+  uint32_t base = fx.before[i];
+  int s = i * a.scan;
+  if (a.scan > 1) {
+    for (int s0 = s, s1 = min(s + a.scan, a.p.num_seqs); s0 < s1; s0 += 32) {
+      uint32_t w = 0u;
+      if (s0 + lane < s1) {
+        const SeqSpan sp = paged_span(a.p, s0 + lane);
+        w = seq_pairs<R>(a, sp) * up_to(seq_rounds(sp), c.unit);
+      }
+      const uint32_t incl = warp_scan(w, lane);
+      const int k = __popc(__ballot_sync(TQ_FULL, base + incl <= c.pos));   // sequences that end before
+      s = min(s0 + k, s1 - 1);
+      if (k < 32) {
+        base += __shfl_sync(TQ_FULL, incl - w, k);
+        break;
+      }
+      base += __shfl_sync(TQ_FULL, incl, 31);
+    }
+  }
+  if (lane == 0) {
+    const bool fresh = c.pos == blockIdx.x * c.per;
+    g.s = s;
+    g.sp = paged_span(a.p, s);
+    const uint32_t rounds = up_to(seq_rounds(g.sp), c.unit), tiles = max(1, (g.sp.n * a.G + R - 1) / R);
+    const uint32_t pair = (c.pos - base) / rounds;
+    g.kvh = min(pair / tiles, a.Hkv - 1);
+    g.lo = pair % tiles * R;
+    const uint32_t r0 = c.pos - base - pair * rounds, n0 = min(c.end - c.pos, rounds - r0);
+    g.g_begin = DW * r0;
+    g.g_end = DW * (r0 + n0);
+    g.rounds = n0;
+    const uint32_t p0 = c.pos - r0, b0 = p0 / c.per;
+    g.parts = (p0 + rounds - 1) / c.per - b0 + 1;
+    g.part = blockIdx.x - b0;
+    g.slot = 2 * blockIdx.x + !fresh;
+    g.slot0 = 2 * b0 + (p0 != b0 * c.per);
+    fx.cut.pos = c.pos + n0;
+  }
+  __syncwarp();
+}
 
 // Bytes of a 32-token group in a ring: key planes, value nibbles (the planes arrive
 // there and are merged in place), scales.
@@ -131,16 +263,7 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
   float *osum = reinterpret_cast<float *>(ring);               // [DW][R][D + 4], once the ring is drained
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x % a.splits, qt = blockIdx.x / a.splits, kvh = blockIdx.y, s = blockIdx.z;
   sm100::pdl_wait();
-  const SeqSpan sp = paged_span(a.p, s);
-  const int lo = qt * R, nrows = min(R, sp.n * a.G - lo);
-  if (nrows <= 0) return;
-  const int vis = tile_visible(sp, a.G, lo, R);
-  const int g_end = min((split + 1) * a.chunk, (vis + 31) >> 5);
-  const int g0 = split * a.chunk + warp;
-  if (split * a.chunk >= g_end && split > 0) return;
-
   const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl, nbv = a.books.bits_v;
   const uint32_t kb = 32 * planes * (D / 8), vb = nbv * D * 4, so = kb + value_room(D);
   const uint32_t stage_bytes = so + 192;
@@ -150,446 +273,481 @@ __global__ void __launch_bounds__(DW * 32, NT <= 2 ? 2 : 1) paged_decode_kernel(
     for (int i = 0; i < a.stages; ++i) sm100::mbar_init(&bar[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncwarp();
-  const int cnt = g_end > g0 ? (g_end - g0 + DW - 1) / DW : 0;   // this warp's groups
+  if (warp == 0) cut_work<R>(a, fx, lane);
   const int P = 1 << a.p.page_shift;
-  int pages = -1;          // lane i: page of group i of the current 32
-  uint32_t valid = 0u, phase = 0u;
-  auto issue = [&](int i, int st) {
-    if ((i & 31) == 0) {
-      const int gi = g0 + (i + lane) * DW;
-      pages = i + lane < cnt ? paged_page(a.p, s, gi * 32) : -1;
-    }
-    const int page = __shfl_sync(TQ_FULL, pages, i & 31);
-    valid = page >= 0 ? valid | (1u << st) : valid & ~(1u << st);
-    if (page >= 0 && lane == 0) {
-      const int64_t row = (static_cast<int64_t>(page) * a.Hkv + kvh) * P + (((g0 + i * DW) * 32) & (P - 1));
-      uint8_t *dst = mine + st * stage_bytes;
-      sm100::mbar_expect_tx(&bar[st], kb + vb + 192);
-      sm100::bulk_g2s(dst, a.kcode + row * planes * (D / 8), kb, &bar[st]);
-      sm100::bulk_g2s(dst + kb, a.vcode + (row >> 5) * nbv * D, vb, &bar[st]);
-      sm100::bulk_g2s(dst + so, a.kscale + row * 2, 128, &bar[st]);
-      sm100::bulk_g2s(dst + so + 128, a.vnorm + row, 64, &bar[st]);
-    }
-  };
-  int issued = 0;
+  uint32_t phase = 0u;
+  bool ok = true;
 #pragma unroll 1
-  for (; issued < a.stages && issued < cnt; ++issued) issue(issued, issued);
-
-  // ---- queries, while the first groups arrive.  q' by warps (rows w, w + 8, ..),
-  // put straight into the code operand and, in two bf16 terms, into the operand of
-  // q'' = S q'
-#pragma unroll 1
-  for (int r = warp; r < R; r += DW) {
-    float x[1][NPL];
-    const int tok = (lo + r) / a.G, at[1] = {sp.len - sp.n + tok};
-    const int64_t off[1] = {r < nrows && at[0] >= 0 ? static_cast<int64_t>(sp.row0 + tok) * a.st +
-                                                          (kvh * a.G + (lo + r) % a.G) * a.sh
-                                                    : -1};
-    paged_load_rows<1, NPL>(x, a.q, off, a.dtype, lane);
-    paged_rope_rows<1, NPL>(x, a.rc, a.rs, at, off, lane);
-    float f = 1.f;
-    if (a.books.pi != nullptr) {
-      tq_warp_dense<NPL>(x[0], a.books.pi_t, fx.scr + warp * D, lane);
-    } else {
-      tq_apply_signs<NPL>(x[0], a.books.dneg, lane);
-      tq_warp_wht<NPL, true>(x[0], lane);
-      f = 1.0f / sqrtf(static_cast<float>(D));
-    }
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      x[0][k] *= f;
-      m = fmaxf(m, fabsf(x[0][k]));
-    }
-    m = tq_warp_max(m);
-    const int e = pow2_above(m);
-    const float down = pow2(-e);
-    if (lane == 0) fx.e1[r] = pow2(e);
-    __half *dst = reinterpret_cast<__half *>(bc + (r >> 3) * 32 + 4 * (r & 7));
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      const int c = lane + 32 * k;
-      // k-step, register, half, thread column of coordinate c
-      const int el = D == 128 ? (c & 31) >> 2 : (c & 15) >> 2, tt = D == 128 ? c >> 5 : c >> 4;
-      const int ks = D == 128 ? 2 * (c & 3) + (el >> 2) : c & 3;
-      dst[(ks * NT * 32 + tt) * 4 + (el & 3)] = __float2half_rn(x[0][k] * down);
-      const __nv_bfloat16 h = __float2bfloat16_rn(x[0][k]);
-      fx.qh[r * Fx::QP + c] = h;
-      fx.ql[r * Fx::QP + c] = __float2bfloat16_rn(x[0][k] - __bfloat162float(h));
-    }
-  }
-  __syncthreads();
-  // q'': warp w takes rows 16 w .. 16 w + 15 of S (d = 64: the first four warps)
-  float z[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[n][e] = 0.f;
-  const bool sk = a.books.qjl && 16 * warp < D;
-  if (sk) {
-    const uint32_t *sr = reinterpret_cast<const uint32_t *>(a.S) + ((16 * warp + g) * D >> 1) + t;
-#pragma unroll 2
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint32_t a0 = sr[8 * ks], a1 = sr[8 * ks + 4 * D], a2 = sr[8 * ks + 4], a3 = sr[8 * ks + 4 * D + 4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const uint32_t *q = reinterpret_cast<const uint32_t *>((term ? fx.ql : fx.qh) + (8 * n + g) * Fx::QP) + 8 * ks + t;
-          asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-              "{%0,%1,%2,%3};"
-              : "+f"(z[n][0]), "+f"(z[n][1]), "+f"(z[n][2]), "+f"(z[n][3])
-              : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(q[0]), "r"(q[4]));
-        }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mx = fmaxf(fabsf(z[n][e]), fabsf(z[n][e + 2])), su = z[n][e] + z[n][e + 2];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
-        su += __shfl_xor_sync(TQ_FULL, su, o);
+  for (;;) {
+    if (warp == 0) next_segment<R>(a, fx, lane);
+    __syncthreads();
+    if (fx.seg.rounds == 0u) break;
+    const SeqSpan sp = fx.seg.sp;
+    const int s = fx.seg.s, kvh = fx.seg.kvh, lo = fx.seg.lo, nrows = min(R, sp.n * a.G - lo);
+    const int g_end = min(fx.seg.g_end, (tile_visible(sp, a.G, lo, R) + 31) >> 5), g0 = fx.seg.g_begin + warp;
+    const int cnt = ok && g_end > g0 ? (g_end - g0 + DW - 1) / DW : 0;   // this warp's groups
+    int pages = -1;          // lane i: page of group i of the current 32
+    uint32_t valid = 0u;
+    auto issue = [&](int i, int st) {
+      if ((i & 31) == 0) {
+        const int gi = g0 + (i + lane) * DW;
+        pages = i + lane < cnt ? paged_page(a.p, s, gi * 32) : -1;
       }
-      if (g == 0) fx.red[warp * R + 8 * n + 2 * t + e] = make_float2(mx, su);
-    }
-  __syncthreads();
+      const int page = __shfl_sync(TQ_FULL, pages, i & 31);
+      valid = page >= 0 ? valid | (1u << st) : valid & ~(1u << st);
+      if (page >= 0 && lane == 0) {
+        const int64_t row = (static_cast<int64_t>(page) * a.Hkv + kvh) * P + (((g0 + i * DW) * 32) & (P - 1));
+        uint8_t *dst = mine + st * stage_bytes;
+        sm100::mbar_expect_tx(&bar[st], kb + vb + 192);
+        sm100::bulk_g2s(dst, a.kcode + row * planes * (D / 8), kb, &bar[st]);
+        sm100::bulk_g2s(dst + kb, a.vcode + (row >> 5) * nbv * D, vb, &bar[st]);
+        sm100::bulk_g2s(dst + so, a.kscale + row * 2, 128, &bar[st]);
+        sm100::bulk_g2s(dst + so + 128, a.vnorm + row, 64, &bar[st]);
+      }
+    };
+    int issued = 0;
 #pragma unroll 1
-  for (int i = 0; i < 2 * NT; ++i) {
-    // column 8 (i / 2) + 2 t + i % 2
-    const int col = 8 * (i >> 1) + 2 * t + (i & 1);
-    float mx = 0.f, su = 0.f;
+    for (; issued < a.stages && issued < cnt; ++issued) issue(issued, issued);
+
+    // ---- queries, while the first groups arrive.  q' by warps (rows w, w + 8, ..),
+    // put straight into the code operand and, in two bf16 terms, into the operand of
+    // q'' = S q'.  All rows and the warp's rows of S are loaded before any is used.
+    const bool sk = a.books.qjl && 16 * warp < D;
+    float x[NT][NPL];
+    {
+      int64_t off[NT];
+      int at[NT];
 #pragma unroll
-    for (int w = 0; w < DW; ++w) {
-      mx = fmaxf(mx, fx.red[w * R + col].x);
-      su += fx.red[w * R + col].y;
+      for (int z = 0; z < NT; ++z) {
+        const int r = warp + DW * z, tok = (lo + r) / a.G;
+        at[z] = sp.len - sp.n + tok;
+        off[z] = r < nrows && at[z] >= 0 ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + (lo + r) % a.G) * a.sh : -1;
+      }
+      paged_load_rows<NT, NPL>(x, a.q, off, a.dtype, lane);
+      paged_rope_rows<NT, NPL>(x, a.rc, a.rs, at, off, lane);
     }
-    const int e = pow2_above(mx);
-    if (sk) {
+    // (several rows wait where their two bf16 terms will go, so that the loop stays rolled)
+    if (NT > 1)
+#pragma unroll
+      for (int z = 0; z < NT; ++z)
+#pragma unroll
+        for (int k = 0; k < NPL; ++k)
+          reinterpret_cast<float *>((k < NPL / 2 ? fx.qh : fx.ql) + (warp + DW * z) * Fx::QP)[lane + 32 * (k % (NPL / 2))] = x[z][k];
+#pragma unroll 1
+    for (int r = warp; r < R; r += DW) {
+      if (NT > 1) {
+#pragma unroll
+        for (int k = 0; k < NPL; ++k)
+          x[0][k] = reinterpret_cast<const float *>((k < NPL / 2 ? fx.qh : fx.ql) + r * Fx::QP)[lane + 32 * (k % (NPL / 2))];
+        __syncwarp();
+      }
+      float f = 1.f;
+      if (a.books.pi != nullptr) {
+        tq_warp_dense<NPL>(x[0], a.books.pi_t, fx.scr + warp * D, lane);
+      } else {
+        tq_apply_signs<NPL>(x[0], a.books.dneg, lane);
+        tq_warp_wht<NPL, true>(x[0], lane);
+        f = 1.0f / sqrtf(static_cast<float>(D));
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        x[0][k] *= f;
+        m = fmaxf(m, fabsf(x[0][k]));
+      }
+      m = tq_warp_max(m);
+      const int e = pow2_above(m);
       const float down = pow2(-e);
+      if (lane == 0) fx.e1[r] = pow2(e);
+      __half *dst = reinterpret_cast<__half *>(bc + (r >> 3) * 32 + 4 * (r & 7));
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float zv = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) zv = i == 2 * n + b ? z[n][2 * q + b] : zv;
-        const int c = 16 * warp + g + 8 * q;       // coordinate
-        const int y = D == 128 ? c & 31 : c & 15, x = D == 128 ? y & 15 : y & 7, tt = D == 128 ? c >> 5 : c >> 4;
-        // 1 / (F_SIGN times the operand value of bit x); bit 15 is shifted down to bit 0
-        const float up = __uint_as_float(0x7f000000u - __float_as_uint(F_SIGN * bit_value(x & (x == 15 ? 0 : 15))));
-        reinterpret_cast<__half *>(bs + ((x >> 1) * NT + (col >> 3)) * 32 + 4 * (col & 7) + tt)[2 * (x & 1) +
-                                                                                                (D == 128 ? y >> 4 : y >> 3)] =
-            __float2half_rn(zv * down * up);
+      for (int k = 0; k < NPL; ++k) {
+        const int c = lane + 32 * k;
+        // k-step, register, half, thread column of coordinate c
+        const int el = D == 128 ? (c & 31) >> 2 : (c & 15) >> 2, tt = D == 128 ? c >> 5 : c >> 4;
+        const int ks = D == 128 ? 2 * (c & 3) + (el >> 2) : c & 3;
+        dst[(ks * NT * 32 + tt) * 4 + (el & 3)] = __float2half_rn(x[0][k] * down);
+        const __nv_bfloat16 h = __float2bfloat16_rn(x[0][k]);
+        fx.qh[r * Fx::QP + c] = h;
+        fx.ql[r * Fx::QP + c] = __float2bfloat16_rn(x[0][k] - __bfloat162float(h));
       }
     }
-    if (warp == 0 && g == 0) {
-      const float sl = a.scale * 1.4426950408889634f;
-      const int pos = sp.len - sp.n + (lo + col) / a.G;
-      colc[col] = make_float4(sl * fx.e1[col], sl * 2.f * a.qjl_coef * F_SIGN * pow2(e), sl * a.qjl_coef * su,
-                              __int_as_float(col < nrows ? pos : -1));
-    }
-  }
-  __syncthreads();
-  sm100::pdl_trigger();
-
-  // ---- groups of 32 tokens, 16 (h = 0, 1) at a time.  Row g of block b (b = 0, 1) of
-  // the logits is token 8 (2 h + b) + 4 (g & 1) + g / 2: the order in which the value
-  // operand holds tokens.
-  float acc_o[MT][NT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
+    __syncthreads();
+    // q'': warp w takes rows 16 w .. 16 w + 15 of S (d = 64: the first four warps)
+    float z[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc_o[i][n][e] = 0.f;
-  float M[NT][2], den[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      M[n][e] = -1e30f;
-      den[n][e] = 0.f;
-    }
-  // the smallest position of the tile's rows: its first token's
-  const int limit_min = sp.len - sp.n + lo / a.G;
-  const int tok0 = 4 * (g & 1) + (g >> 1);
-  bool ok = true;
-  int stg = 0;
-#pragma unroll 1
-  for (int i = 0; i < cnt; ++i) {
-    if ((valid >> stg) & 1u) {
-      ok = __all_sync(TQ_FULL, sm100::mbar_wait(&bar[stg], (phase >> stg) & 1u, a.wait_limit));
-      if (!ok) break;
-      phase ^= 1u << stg;
-      uint8_t *base = mine + stg * stage_bytes;
-      const int j0 = (g0 + i * DW) * 32;
-      // ---- value planes to nibbles: the words of coordinates NPL lane .. of all
-      // planes become, for both halves h and the four shifts s, pairs of 4-token nibble
-      // runs of two neighbouring coordinates
-      {
-        uint32_t *vw = reinterpret_cast<uint32_t *>(base + kb);
-        uint32_t w[NPL][4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if (NPL == 4) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (p < nbv) v = *reinterpret_cast<const uint4 *>(vw + p * D + 4 * lane);
-            w[0][p] = v.x;
-            w[1][p] = v.y;
-            w[NPL - 2][p] = v.z;
-            w[NPL - 1][p] = v.w;
-          } else {
-            uint2 v = make_uint2(0u, 0u);
-            if (p < nbv) v = *reinterpret_cast<const uint2 *>(vw + p * D + 2 * lane);
-            w[0][p] = v.x;
-            w[1][p] = v.y;
-          }
-        }
-        __syncwarp();
-        uint32_t nb[NPL][4];
-#pragma unroll
-        for (int c = 0; c < NPL; ++c) nibbles4<V4>(w[c], nb[c]);
-#pragma unroll
-        for (int sft = 0; sft < 4; ++sft)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t sel = h ? 0x7632 : 0x5410;
-            uint32_t *o = vw + (4 * h + sft) * VS + (NPL / 2) * lane;
-            if (NPL == 4)
-              *reinterpret_cast<uint2 *>(o) =
-                  make_uint2(prmt(nb[0][sft], nb[1][sft], sel), prmt(nb[NPL - 2][sft], nb[NPL - 1][sft], sel));
-            else
-              *o = prmt(nb[0][sft], nb[1][sft], sel);
-          }
-        __syncwarp();
-      }
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        // ---- logits
-        float s1[NT][4], s2[NT][4];
+      for (int e = 0; e < 4; ++e) z[n][e] = 0.f;
+    if (sk) {
+      const uint32_t *sr = reinterpret_cast<const uint32_t *>(a.S) + ((16 * warp + g) * D >> 1) + t;
+#pragma unroll 2
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t a0 = sr[8 * ks], a1 = sr[8 * ks + 4 * D], a2 = sr[8 * ks + 4], a3 = sr[8 * ks + 4 * D + 4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s1[n][e] = s2[n][e] = 0.f;
-        uint32_t nb[2][4], sg[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t *kr = reinterpret_cast<const uint32_t *>(base) + (8 * (2 * h + b) + tok0) * planes * NPL +
-                               (D == 128 ? t : t >> 1);
-          uint32_t w[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) w[p] = p < mbk ? kr[p * NPL] : 0u;
-          sg[b] = a.books.qjl ? kr[mbk * NPL] : 0u;
-          if (D == 64) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) w[p] >>= 16 * (t & 1);
-            sg[b] = prmt(sg[b], 0u, t & 1 ? 0x4342 : 0x4140);
+          for (int term = 0; term < 2; ++term) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>((term ? fx.ql : fx.qh) + (8 * n + g) * Fx::QP) + 8 * ks + t;
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                "{%0,%1,%2,%3};"
+                : "+f"(z[n][0]), "+f"(z[n][1]), "+f"(z[n][2]), "+f"(z[n][3])
+                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(q[0]), "r"(q[4]));
           }
-          nibbles4<K4>(w, nb[b]);
-        }
-#pragma unroll
-        for (int sft = 0; sft < 4; ++sft) {
-          uint32_t oa[4], ob[4];
-          expand8<K4>(nb[0][sft], a.lutk, oa);
-          expand8<K4>(nb[1][sft], a.lutk, ob);
-#pragma unroll
-          for (int hf = 0; hf < (D == 128 ? 2 : 1); ++hf) {
-            const int ks = D == 128 ? 2 * sft + hf : sft;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint2 b = bc[(ks * NT + n) * 32 + lane];
-              mma16816(s1[n], oa[2 * hf], ob[2 * hf], oa[2 * hf + 1], ob[2 * hf + 1], b.x, b.y);
-            }
-          }
-        }
-        if (a.books.qjl) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            uint32_t ar[2][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const int x = 2 * ks + r;
-                ar[b][r] = x == 15 ? (sg[b] >> 15) & 0x00010001u : sg[b] & (0x00010001u << x);
-              }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint2 b = bs[(ks * NT + n) * 32 + lane];
-              mma16816(s2[n], ar[0][0], ar[1][0], ar[0][1], ar[1][1], b.x, b.y);
-            }
-          }
-        }
-        // ---- logits in units of log2, value norm added; the largest of each column
-        float lg[NT][4], inv[2], top[NT][2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int tk = 8 * (2 * h + b) + tok0;
-          const uint32_t sc = reinterpret_cast<const uint32_t *>(base + so)[tk];
-          const float nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
-          const float rho = tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
-          // (a NaN behind the sequence's end becomes the floor)
-          const float nv = fmaxf(tq_half_to_f32(reinterpret_cast<const uint16_t *>(base + so + 128)[tk]), 5.9604645e-8f);
-          const float lnv = __log2f(nv);
-          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[b]) : "f"(nv));
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float4 cc = colc[n * 8 + 2 * t + e];
-              lg[n][2 * b + e] =
-                  fmaf(nu, fmaf(cc.x, s1[n][2 * b + e], rho * fmaf(cc.y, s2[n][2 * b + e], -cc.z)), lnv);
-            }
-        }
-        if (j0 + 31 > limit_min) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j0 + 8 * (2 * h + (e >> 1)) + tok0 > __float_as_int(colc[n * 8 + 2 * t + (e & 1)].w))
-                lg[n][e] = -CUDART_INF_F;
-        }
-        bool grow = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            top[n][e] = fmaxf(lg[n][e], lg[n][e + 2]);
-            grow |= top[n][e] > M[n][e] + 8.f;
-          }
-        // ---- reference of the weights: moved only when a weight would exceed 2^8
-        // (fp16 weights are as exact there as at 1)
-        if (__any_sync(TQ_FULL, grow)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = top[n][e];
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
-              const float mn = fmaxf(M[n][e], mx), corr = ex2(M[n][e] - mn);
-              M[n][e] = mn;
-              den[n][e] *= corr;
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                acc_o[m][n][e] *= corr;
-                acc_o[m][n][e + 2] *= corr;
-              }
-            }
-        }
-        uint32_t pf[2][NT];      // weights as operand registers of the values
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float e[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              e[c] = ex2(lg[n][2 * b + c] - M[n][c]);
-              den[n][c] = fmaf(e[c], inv[b], den[n][c]);
-            }
-            const __half2 hv = __floats2half2_rn(e[0], e[1]);
-            pf[b][n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&hv));
-          }
-        // ---- values: rows g and g + 8 of m-tile 2 c4 + m are coordinates 32 c4 + 4 g +
-        // 2 m and the next
-        const uint32_t *vn = reinterpret_cast<const uint32_t *>(base + kb) + (4 * h + t) * VS + 2 * g;
-#pragma unroll
-        for (int c4 = 0; c4 < NPL; ++c4) {
-          const uint2 v = *reinterpret_cast<const uint2 *>(vn + 16 * c4);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint32_t o[4];
-            expand8<V4>(m ? v.y : v.x, a.lutv, o);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(acc_o[2 * c4 + m][n], o[0], o[2], o[1], o[3], pf[0][n], pf[1][n]);
-          }
-        }
       }
-      __syncwarp();
     }
-    if (issued < cnt) {
-      // the merged nibbles were written by threads, the next copy by the copy engine
-      sm100::fence_async_smem();
-      __syncwarp();
-      issue(issued, stg);
-      ++issued;
-    } else {
-      valid &= ~(1u << stg);      // nothing of this slot is awaited any more
-    }
-    stg = stg + 1 == a.stages ? 0 : stg + 1;
-  }
-  if (!ok) {
-    // a copy never arrived: let the others land, and answer NaN
-    for (int i = 0; i < a.stages; ++i)
-      if ((valid >> i) & 1u) sm100::mbar_wait(&bar[i], (phase >> i) & 1u, 1u << 20);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        M[n][e] = 0.f;
-        den[n][e] = CUDART_NAN_F;
+        float mx = fmaxf(fabsf(z[n][e]), fabsf(z[n][e + 2])), su = z[n][e] + z[n][e + 2];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+          su += __shfl_xor_sync(TQ_FULL, su, o);
+        }
+        if (g == 0) fx.red[warp * R + 8 * n + 2 * t + e] = make_float2(mx, su);
       }
-  }
-  // ---- the block's sums: rescale to the common reference, add the warps
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < 2 * NT; ++i) {
+      // column 8 (i / 2) + 2 t + i % 2
+      const int col = 8 * (i >> 1) + 2 * t + (i & 1);
+      float mx = 0.f, su = 0.f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+      for (int w = 0; w < DW; ++w) {
+        mx = fmaxf(mx, fx.red[w * R + col].x);
+        su += fx.red[w * R + col].y;
+      }
+      const int e = pow2_above(mx);
+      if (sk) {
+        const float down = pow2(-e);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+        for (int q = 0; q < 2; ++q) {
+          float zv = 0.f;
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) den[n][e] += __shfl_xor_sync(TQ_FULL, den[n][e], o);
-      if (g == 0) {
-        sM[warp * R + n * 8 + 2 * t + e] = M[n][e];
-        sM[(DW + warp) * R + n * 8 + 2 * t + e] = den[n][e];
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) zv = i == 2 * n + b ? z[n][2 * q + b] : zv;
+          const int c = 16 * warp + g + 8 * q;       // coordinate
+          const int y = D == 128 ? c & 31 : c & 15, x = D == 128 ? y & 15 : y & 7, tt = D == 128 ? c >> 5 : c >> 4;
+          // 1 / (F_SIGN times the operand value of bit x); bit 15 is shifted down to bit 0
+          const float up = __uint_as_float(0x7f000000u - __float_as_uint(F_SIGN * bit_value(x & (x == 15 ? 0 : 15))));
+          reinterpret_cast<__half *>(bs + ((x >> 1) * NT + (col >> 3)) * 32 + 4 * (col & 7) + tt)[2 * (x & 1) +
+                                                                                                  (D == 128 ? y >> 4 : y >> 3)] =
+              __float2half_rn(zv * down * up);
+        }
+      }
+      if (warp == 0 && g == 0) {
+        const float sl = a.scale * 1.4426950408889634f;
+        const int pos = sp.len - sp.n + (lo + col) / a.G;
+        colc[col] = make_float4(sl * fx.e1[col], sl * 2.f * a.qjl_coef * F_SIGN * pow2(e), sl * a.qjl_coef * su,
+                                __int_as_float(col < nrows ? pos : -1));
       }
     }
-  __syncthreads();     // every warp is past its ring as well
+    __syncthreads();
+    sm100::pdl_trigger();
+
+    // ---- groups of 32 tokens, 16 (h = 0, 1) at a time.  Row g of block b (b = 0, 1) of
+    // the logits is token 8 (2 h + b) + 4 (g & 1) + g / 2: the order in which the value
+    // operand holds tokens.
+    float acc_o[MT][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int col = n * 8 + 2 * t + e;
-      float mx = sM[col];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + col]);
-      const float f = ex2(M[n][e] - mx);
+        for (int e = 0; e < 4; ++e) acc_o[i][n][e] = 0.f;
+    float M[NT][2], den[NT][2];
 #pragma unroll
-      for (int c4 = 0; c4 < NPL; ++c4)
-        *reinterpret_cast<float4 *>(osum + (warp * R + col) * (D + 4) + 32 * c4 + 4 * g) =
-            make_float4(acc_o[2 * c4][n][e] * f, acc_o[2 * c4][n][e + 2] * f, acc_o[2 * c4 + 1][n][e] * f,
-                        acc_o[2 * c4 + 1][n][e + 2] * f);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        M[n][e] = -1e30f;
+        den[n][e] = 0.f;
+      }
+    // the smallest position of the tile's rows: its first token's
+    const int limit_min = sp.len - sp.n + lo / a.G;
+    const int tok0 = 4 * (g & 1) + (g >> 1);
+    int stg = 0;
+#pragma unroll 1
+    for (int i = 0; i < cnt; ++i) {
+      if ((valid >> stg) & 1u) {
+        ok = __all_sync(TQ_FULL, sm100::mbar_wait(&bar[stg], (phase >> stg) & 1u, a.wait_limit));
+        if (!ok) break;
+        phase ^= 1u << stg;
+        uint8_t *base = mine + stg * stage_bytes;
+        const int j0 = (g0 + i * DW) * 32;
+        // ---- value planes to nibbles: the words of coordinates NPL lane .. of all
+        // planes become, for both halves h and the four shifts s, pairs of 4-token nibble
+        // runs of two neighbouring coordinates
+        {
+          uint32_t *vw = reinterpret_cast<uint32_t *>(base + kb);
+          uint32_t w[NPL][4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            if (NPL == 4) {
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (p < nbv) v = *reinterpret_cast<const uint4 *>(vw + p * D + 4 * lane);
+              w[0][p] = v.x;
+              w[1][p] = v.y;
+              w[NPL - 2][p] = v.z;
+              w[NPL - 1][p] = v.w;
+            } else {
+              uint2 v = make_uint2(0u, 0u);
+              if (p < nbv) v = *reinterpret_cast<const uint2 *>(vw + p * D + 2 * lane);
+              w[0][p] = v.x;
+              w[1][p] = v.y;
+            }
+          }
+          __syncwarp();
+          uint32_t nb[NPL][4];
+#pragma unroll
+          for (int c = 0; c < NPL; ++c) nibbles4<V4>(w[c], nb[c]);
+#pragma unroll
+          for (int sft = 0; sft < 4; ++sft)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t sel = h ? 0x7632 : 0x5410;
+              uint32_t *o = vw + (4 * h + sft) * VS + (NPL / 2) * lane;
+              if (NPL == 4)
+                *reinterpret_cast<uint2 *>(o) =
+                    make_uint2(prmt(nb[0][sft], nb[1][sft], sel), prmt(nb[NPL - 2][sft], nb[NPL - 1][sft], sel));
+              else
+                *o = prmt(nb[0][sft], nb[1][sft], sel);
+            }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          // ---- logits
+          float s1[NT][4], s2[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s1[n][e] = s2[n][e] = 0.f;
+          uint32_t nb[2][4], sg[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t *kr = reinterpret_cast<const uint32_t *>(base) + (8 * (2 * h + b) + tok0) * planes * NPL +
+                                 (D == 128 ? t : t >> 1);
+            uint32_t w[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) w[p] = p < mbk ? kr[p * NPL] : 0u;
+            sg[b] = a.books.qjl ? kr[mbk * NPL] : 0u;
+            if (D == 64) {
+#pragma unroll
+              for (int p = 0; p < 4; ++p) w[p] >>= 16 * (t & 1);
+              sg[b] = prmt(sg[b], 0u, t & 1 ? 0x4342 : 0x4140);
+            }
+            nibbles4<K4>(w, nb[b]);
+          }
+#pragma unroll
+          for (int sft = 0; sft < 4; ++sft) {
+            uint32_t oa[4], ob[4];
+            expand8<K4>(nb[0][sft], a.lutk, oa);
+            expand8<K4>(nb[1][sft], a.lutk, ob);
+#pragma unroll
+            for (int hf = 0; hf < (D == 128 ? 2 : 1); ++hf) {
+              const int ks = D == 128 ? 2 * sft + hf : sft;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint2 b = bc[(ks * NT + n) * 32 + lane];
+                mma16816(s1[n], oa[2 * hf], ob[2 * hf], oa[2 * hf + 1], ob[2 * hf + 1], b.x, b.y);
+              }
+            }
+          }
+          if (a.books.qjl) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              uint32_t ar[2][2];
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int x = 2 * ks + r;
+                  ar[b][r] = x == 15 ? (sg[b] >> 15) & 0x00010001u : sg[b] & (0x00010001u << x);
+                }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint2 b = bs[(ks * NT + n) * 32 + lane];
+                mma16816(s2[n], ar[0][0], ar[1][0], ar[0][1], ar[1][1], b.x, b.y);
+              }
+            }
+          }
+          // ---- logits in units of log2, value norm added; the largest of each column
+          float lg[NT][4], inv[2], top[NT][2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int tk = 8 * (2 * h + b) + tok0;
+            const uint32_t sc = reinterpret_cast<const uint32_t *>(base + so)[tk];
+            const float nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+            const float rho = tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
+            // (a NaN behind the sequence's end becomes the floor)
+            const float nv = fmaxf(tq_half_to_f32(reinterpret_cast<const uint16_t *>(base + so + 128)[tk]), 5.9604645e-8f);
+            const float lnv = __log2f(nv);
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[b]) : "f"(nv));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float4 cc = colc[n * 8 + 2 * t + e];
+                lg[n][2 * b + e] =
+                    fmaf(nu, fmaf(cc.x, s1[n][2 * b + e], rho * fmaf(cc.y, s2[n][2 * b + e], -cc.z)), lnv);
+              }
+          }
+          if (j0 + 31 > limit_min) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (j0 + 8 * (2 * h + (e >> 1)) + tok0 > __float_as_int(colc[n * 8 + 2 * t + (e & 1)].w))
+                  lg[n][e] = -CUDART_INF_F;
+          }
+          bool grow = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              top[n][e] = fmaxf(lg[n][e], lg[n][e + 2]);
+              grow |= top[n][e] > M[n][e] + 8.f;
+            }
+          // ---- reference of the weights: moved only when a weight would exceed 2^8
+          // (fp16 weights are as exact there as at 1)
+          if (__any_sync(TQ_FULL, grow)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mx = top[n][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(TQ_FULL, mx, o));
+                const float mn = fmaxf(M[n][e], mx), corr = ex2(M[n][e] - mn);
+                M[n][e] = mn;
+                den[n][e] *= corr;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  acc_o[m][n][e] *= corr;
+                  acc_o[m][n][e + 2] *= corr;
+                }
+              }
+          }
+          uint32_t pf[2][NT];      // weights as operand registers of the values
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float e[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                e[c] = ex2(lg[n][2 * b + c] - M[n][c]);
+                den[n][c] = fmaf(e[c], inv[b], den[n][c]);
+              }
+              const __half2 hv = __floats2half2_rn(e[0], e[1]);
+              pf[b][n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&hv));
+            }
+          // ---- values: rows g and g + 8 of m-tile 2 c4 + m are coordinates 32 c4 + 4 g +
+          // 2 m and the next
+          const uint32_t *vn = reinterpret_cast<const uint32_t *>(base + kb) + (4 * h + t) * VS + 2 * g;
+#pragma unroll
+          for (int c4 = 0; c4 < NPL; ++c4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(vn + 16 * c4);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              uint32_t o[4];
+              expand8<V4>(m ? v.y : v.x, a.lutv, o);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816(acc_o[2 * c4 + m][n], o[0], o[2], o[1], o[3], pf[0][n], pf[1][n]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (issued < cnt) {
+        // the merged nibbles were written by threads, the next copy by the copy engine
+        sm100::fence_async_smem();
+        __syncwarp();
+        issue(issued, stg);
+        ++issued;
+      } else {
+        valid &= ~(1u << stg);      // nothing of this slot is awaited any more
+      }
+      stg = stg + 1 == a.stages ? 0 : stg + 1;
     }
-  __syncthreads();
-  for (int r = warp; r < nrows; r += DW) {
-    float mx = sM[r];
+    if (!ok) {
+      // a copy never arrived: let the others land, and answer NaN
+      for (int i = 0; i < a.stages; ++i)
+        if ((valid >> i) & 1u) sm100::mbar_wait(&bar[i], (phase >> i) & 1u, 1u << 20);
 #pragma unroll
-    for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + r]);
-    float l = 0.f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int w = 0; w < DW; ++w) l += sM[(DW + w) * R + r] * ex2(sM[w * R + r] - mx);
-    float x[NPL];
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      x[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < DW; ++w) x[k] += osum[(w * R + r) * (D + 4) + lane + 32 * k];
+        for (int e = 0; e < 2; ++e) {
+          M[n][e] = 0.f;
+          den[n][e] = CUDART_NAN_F;
+        }
     }
-    const int64_t row = static_cast<int64_t>(sp.row0 + (lo + r) / a.G) * a.Hq + kvh * a.G + (lo + r) % a.G;
-    if (a.splits > 1) {
+    // ---- the block's sums: rescale to the common reference, add the warps
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) a.po[(row * a.splits + split) * D + lane + 32 * k] = x[k];
-      if (lane == 0) a.pml[row * a.splits + split] = make_float2(mx, l);
-    } else {
-      paged_store_row<D>(x, l, a.books, osum + r * (D + 4), a.out, a.out_dtype, row, lane);
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) den[n][e] += __shfl_xor_sync(TQ_FULL, den[n][e], o);
+        if (g == 0) {
+          sM[warp * R + n * 8 + 2 * t + e] = M[n][e];
+          sM[(DW + warp) * R + n * 8 + 2 * t + e] = den[n][e];
+        }
+      }
+    __syncthreads();     // every warp is past its ring as well
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = n * 8 + 2 * t + e;
+        float mx = sM[col];
+#pragma unroll
+        for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + col]);
+        const float f = ex2(M[n][e] - mx);
+#pragma unroll
+        for (int c4 = 0; c4 < NPL; ++c4)
+          *reinterpret_cast<float4 *>(osum + (warp * R + col) * (D + 4) + 32 * c4 + 4 * g) =
+              make_float4(acc_o[2 * c4][n][e] * f, acc_o[2 * c4][n][e + 2] * f, acc_o[2 * c4 + 1][n][e] * f,
+                          acc_o[2 * c4 + 1][n][e + 2] * f);
+      }
+    __syncthreads();
+    for (int r = warp; r < nrows; r += DW) {
+      float mx = sM[r];
+#pragma unroll
+      for (int w = 1; w < DW; ++w) mx = fmaxf(mx, sM[w * R + r]);
+      float l = 0.f;
+#pragma unroll
+      for (int w = 0; w < DW; ++w) l += sM[(DW + w) * R + r] * ex2(sM[w * R + r] - mx);
+      float x[NPL];
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        x[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < DW; ++w) x[k] += osum[(w * R + r) * (D + 4) + lane + 32 * k];
+      }
+      const int64_t row = static_cast<int64_t>(sp.row0 + (lo + r) / a.G) * a.Hq + kvh * a.G + (lo + r) % a.G;
+      const Segment &sg = fx.seg;
+      if (sg.part == 0 && lane == 0) a.info[row] = make_int2(sg.slot0, sg.parts);
+      if (sg.parts > 1) {
+        const int64_t at = static_cast<int64_t>(sg.slot) * R + r;
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) a.po[at * D + lane + 32 * k] = x[k];
+        if (lane == 0) a.pml[at] = make_float2(mx, l);
+      } else {
+        paged_store_row<D>(x, l, a.books, osum + r * (D + 4), a.out, a.out_dtype, row, lane);
+      }
     }
+    // the ring, written by threads, goes back to the copy engine
+    sm100::fence_async_smem();
+    __syncthreads();
   }
 }
 
-// One block per answer row: the splits' sums joined (a warp every fourth split, a lane
+// One block per answer row: the parts' sums joined (a warp every fourth part, a lane
 // D / 32 neighbouring coordinates), rotated back, stored.
 template <int D>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ DecArgs a, int R) {
@@ -599,33 +757,35 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = blockIdx.x;
   sm100::pdl_wait();
+  const int2 info = a.info[row];      // (anything where the row belongs to no sequence)
   const int tok = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
   const int s = paged_find_seq(a.p, tok, 1, 0);
   const SeqSpan sp = paged_span(a.p, s);
   const int i = tok - sp.row0;
   if (i < 0 || i >= sp.n) return;
-  const int vis = tile_visible(sp, a.G, (i * a.G + h % a.G) / R * R, R);
-  const int n = max(1, ((vis + 31) / 32 + a.chunk - 1) / a.chunk);
-  const float2 *ml = a.pml + row * a.splits;
+  if (info.y <= 1) return;       // stored by the block that had the whole pair
+  // parts 1 .. are first in their blocks
+  const int r = (i * a.G + h % a.G) % R, b0 = info.x >> 1, n = min(info.y, a.blocks - b0);
+  const auto at = [&](int j) { return static_cast<int64_t>(j == 0 ? info.x : 2 * (b0 + j)) * R + r; };
   float mx = -CUDART_INF_F;
-  for (int j = lane; j < n; j += 32) mx = fmaxf(mx, ml[j].x);
+  for (int j = lane; j < n; j += 32) mx = fmaxf(mx, a.pml[at(j)].x);
   mx = tq_warp_max(mx);
   float l = 0.f, x[NPL];
 #pragma unroll
   for (int k = 0; k < NPL; ++k) x[k] = 0.f;
-  const float *po = a.po + row * a.splits * D + NPL * lane;
+  const float *po = a.po + NPL * lane;
 #pragma unroll 5
   for (int j = warp; j < n; j += 4) {
-    const float2 m = ml[j];
+    const float2 m = a.pml[at(j)];
     float v[NPL];
     if (NPL == 4) {
-      const float4 u = *reinterpret_cast<const float4 *>(po + static_cast<int64_t>(j) * D);
+      const float4 u = *reinterpret_cast<const float4 *>(po + at(j) * D);
       v[0] = u.x;
       v[1] = u.y;
       v[NPL - 2] = u.z;
       v[NPL - 1] = u.w;
     } else {
-      const float2 u = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(j) * D);
+      const float2 u = *reinterpret_cast<const float2 *>(po + at(j) * D);
       v[0] = u.x;
       v[1] = u.y;
     }
@@ -647,7 +807,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
 }
 
 struct DecPlan {
-  int NT, qtiles, chunk, splits, stages;
+  int NT, blocks, stages;
   size_t smem;
 };
 
@@ -659,22 +819,16 @@ size_t fixed_smem(int d, int NT) {
   return (n + 127) / 128 * 128;
 }
 
-// Query rows a tile: 8, 16 or 32.  Blocks: enough for every SM to hold its two
-// (one with 32 rows), but no fewer than 8 groups (one a warp) in a block.
+// Query rows a tile: 8, 16 or 32.  Blocks: as many as the SMs hold (two, one with 32
+// rows), but no fewer than 8 groups (one a warp) in a block.
 DecPlan plan(const tq_codec *c, int num_seqs, int max_new, int max_len, int Hq, int Hkv) {
   DecPlan p;
-  const int rows = max_new * (Hq / Hkv), sms = 148;
+  const int64_t rows = static_cast<int64_t>(max_new) * (Hq / Hkv), sms = 148;
   p.NT = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  p.qtiles = (rows + 8 * p.NT - 1) / (8 * p.NT);
   const int per_sm = p.NT <= 2 ? 2 : 1;
-  const int64_t pairs = static_cast<int64_t>(num_seqs) * Hkv * p.qtiles;
-  const int groups = std::max(1, (max_len + 31) / 32);
-  const int64_t slots = static_cast<int64_t>(sms) * per_sm;
-  int64_t want = pairs >= slots ? (4 * slots + pairs - 1) / pairs : slots / pairs;
-  want = std::min<int64_t>(std::max<int64_t>(want, 1), (groups + DW - 1) / DW);
-  want = std::min<int64_t>(want, 512);
-  p.chunk = static_cast<int>((groups + want - 1) / want);
-  p.splits = (groups + p.chunk - 1) / p.chunk;
+  const int64_t pairs = static_cast<int64_t>(num_seqs) * Hkv * ((rows + 8 * p.NT - 1) / (8 * p.NT));
+  const int64_t rounds = std::max(1, (max_len + 32 * DW - 1) / (32 * DW));
+  p.blocks = static_cast<int>(pairs >= sms * per_sm ? sms * per_sm : std::min(sms * per_sm, pairs * rounds));
   const int planes = c->mse_bits_k + c->qjl_k;
   const size_t stage = 32 * planes * (c->d / 8) + value_room(c->d) + 192;
   const size_t fixed = fixed_smem(c->d, p.NT);
@@ -684,6 +838,9 @@ DecPlan plan(const tq_codec *c, int num_seqs, int max_new, int max_len, int Hq, 
   p.smem = fixed + std::max(DW * p.stages * stage, merge);
   return p;
 }
+
+// Rows of partial sums: a block holds at most two pairs that it shares.
+size_t part_rows(const DecPlan &p) { return static_cast<size_t>(p.blocks) * 2 * 8 * p.NT; }
 
 template <int D, bool K4, bool V4, int NT>
 int run_dec(const DecArgs &a, const DecPlan &pl, cudaStream_t stream) {
@@ -696,11 +853,9 @@ int run_dec(const DecArgs &a, const DecPlan &pl, cudaStream_t stream) {
       return tq_check_launch("cudaFuncSetAttribute(paged_decode)");
     done[dev] = true;
   }
-  const dim3 grid(pl.splits * pl.qtiles, a.Hkv, a.p.num_seqs);
-  if (tq_launch_pdl(kern, grid, dim3(DW * 32), pl.smem, stream, a) != cudaSuccess)
+  if (tq_launch_pdl(kern, dim3(pl.blocks), dim3(DW * 32), pl.smem, stream, a) != cudaSuccess)
     return tq_check_launch("paged_decode_kernel");
   tq_count_launch(1);
-  if (pl.splits == 1) return tq_check_launch("paged_decode_kernel");
   const int64_t rows = static_cast<int64_t>(a.p.N) * a.Hq;
   if (tq_launch_pdl(paged_combine_kernel<D>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, stream, a,
                     8 * NT) != cudaSuccess)
@@ -729,14 +884,17 @@ int run_dec_d(const DecArgs &a, const DecPlan &pl, bool k4, bool v4, cudaStream_
 size_t paged_decode_workspace_bytes(const tq_codec *c, int N, int num_seqs, int max_new, int max_len, int Hq,
                                     int Hkv) {
   const DecPlan p = plan(c, num_seqs, max_new, max_len, Hq, Hkv);
-  if (p.splits == 1) return 16;
-  return static_cast<size_t>(N) * Hq * p.splits * (c->d + 2) * sizeof(float) + 16;
+  return part_rows(p) * (c->d + 2) * sizeof(float) + static_cast<size_t>(N) * Hq * sizeof(int2);
 }
 
 int launch_paged_decode(const tq_codec *c, const PagedView &p, const void *q, int dtype, int64_t st, int64_t sh,
                         int Hq, const tq_cache *cache, float scale, const float *rc, const float *rs, void *ws,
                         void *out, int out_dtype, cudaStream_t stream) {
   const DecPlan pl = plan(c, p.num_seqs, p.max_new, p.max_len, Hq, cache->Hkv);
+  // the work is counted in 32 bits
+  const double tiles = static_cast<double>(p.N) * Hq / (8 * pl.NT) + static_cast<double>(p.num_seqs) * cache->Hkv;
+  if (tiles * ((p.max_len + 32 * DW - 1) / (32 * DW) + 1) > 2147483647.0)
+    return tq_fail(TQ_ERR_INVALID_ARG, "paged_attention: tokens x heads x max_seq_len too large for one call");
   DecArgs a;
   a.p = p;
   a.q = q;
@@ -757,12 +915,12 @@ int launch_paged_decode(const tq_codec *c, const PagedView &p, const void *q, in
   a.out = out;
   a.out_dtype = out_dtype;
   a.S = c->S_dev;
-  a.qtiles = pl.qtiles;
-  a.chunk = pl.chunk;
-  a.splits = pl.splits;
+  a.blocks = pl.blocks;
+  a.scan = (p.num_seqs + 31) / 32;
   a.stages = pl.stages;
   a.po = static_cast<float *>(ws);
-  a.pml = reinterpret_cast<float2 *>(a.po + static_cast<size_t>(p.N) * Hq * pl.splits * c->d);
+  a.pml = reinterpret_cast<float2 *>(a.po + part_rows(pl) * c->d);
+  a.info = reinterpret_cast<int2 *>(a.pml + part_rows(pl));
   a.wait_limit = 1u << 26;
   if (const char *e = getenv("TQ_WAIT_LIMIT")) a.wait_limit = static_cast<uint32_t>(strtoul(e, nullptr, 10));
   byte_table(c->books.ck, c->mse_bits_k, a.lutk);

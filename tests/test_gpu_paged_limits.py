@@ -95,6 +95,46 @@ def test_attention_of_wide_head_groups(G, Hkv, new):
     assert err <= pt.attention_tolerance(sigma, torch.bfloat16), err
 
 
+RAGGED = [
+    # d, Hq, Hkv, sequences, longest, most new tokens
+    (64, 4, 2, 40, 300, 1), (128, 8, 1, 40, 700, 2), (64, 4, 4, 300, 150, 3), (128, 4, 2, 1100, 40, 1),
+    (128, 8, 2, 3, 9000, 6), (64, 6, 2, 5, 5000, 4), (128, 12, 1, 33, 400, 9)]
+
+
+@pytest.mark.parametrize("case", RAGGED, ids=[f"d{c[0]}h{c[1]}-{c[2]}s{c[3]}n{c[5]}" for c in RAGGED])
+def test_ragged_batches_of_few_rows(case):
+    """Sequences of very unequal lengths, some without new tokens, some without
+    any token: work that is cut inside sequences, and blocks with several."""
+    d, Hq, Hkv, S, longest, most = case
+    page = 32
+    ocodec, ncodec = pt.codecs(d, 3, True, 4)
+    g = np.random.default_rng(S)
+    lens = np.maximum(g.integers(-3, longest, S), 0)
+    lens[:3] = longest, 1, 0
+    news = np.minimum(g.integers(0, most + 1, S), lens)
+    news[0] = most
+    news[2] = 1                                    # a token without a position
+    batch = pt.Batch([(int(a), int(b)) for a, b in zip(lens, news)], page, seed=S, start=2, extra_rows=1)
+    planes = pt.random_pages(ocodec, batch.pool, Hkv, page)
+    cache, b = pt.upload(planes, ncodec), batch.device()
+    q = bf16(g, batch.N, Hq, d)
+    got = attend(ncodec, q, cache, b, Hkv, ws_fill=255)
+    out = got.float().cpu().numpy()
+    ref, sigma = pt.attention_ref(planes, ocodec, batch, q.float().cpu().numpy().astype(np.float64),
+                                  1 / math.sqrt(d), None)
+    known = ~np.isnan(ref)
+    assert np.all(out[~known] == 7.0)
+    tol = pt.attention_tolerance(sigma, torch.bfloat16)
+    for r in range(batch.N):
+        for h in range(Hq):
+            if known[r, h, 0]:
+                n, e = np.linalg.norm(ref[r, h]), np.linalg.norm(out[r, h] - ref[r, h])
+                assert e <= 4 * tol * n, (r, h, e, n)
+    assert np.linalg.norm((out - ref)[known]) <= tol * np.linalg.norm(ref[known])
+    # the same again, bit by bit
+    assert torch.equal(attend(ncodec, q, cache, b, Hkv, ws_fill=0), got)
+
+
 @pytest.mark.parametrize("new", [1, 3, 90])
 def test_limits_larger_than_the_call_do_not_change_it(new):
     """max_new and max_seq_len are limits: generous ones give the same rows (the

@@ -203,6 +203,9 @@ def test_row_limits_of_a_call(L, codec):
     for N, Hq in ((1 << 24, 256), ((1 << 24) + 1, 4), (8, 65536 * 2)):
         assert L.tq_paged_attention_workspace(c, ctypes.byref(batch()), N, Hq, 1,
                                               ctypes.byref(n)) == native.TQ_ERR_INVALID_ARG
+    # more work than a call counts: refused before any device work
+    long = batch(num_seqs=65535, max_pages=1 << 24, table_stride=1 << 24, max_new=1, max_seq_len=1 << 30)
+    assert attention(L, c, N=65535, Hq=8, ca=cache(heads=8), b=long) == native.TQ_ERR_INVALID_ARG
     # a limit on new tokens far above the call's tokens counts as the call's
     for Hq in (8, 160):
         sizes = []
