@@ -24,6 +24,7 @@
 // not leave room for two tiles of queries and keys in shared memory.
 #include <math_constants.h>
 
+#include <cmath>
 #include <cstdlib>
 
 #include "paged_expand.cuh"
@@ -950,14 +951,33 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   float l = 0.f, x[NPL];
 #pragma unroll
   for (int k = 0; k < NPL; ++k) x[k] = 0.f;
-#pragma unroll 4
+  // a lane D / 32 neighbouring coordinates
+  const float *po = a.po + row * a.splits * D + NPL * lane;
+#pragma unroll 8
   for (int j = 0; j < n; ++j) {
     const float2 m = ml[j];
+    float v[NPL];
+    if (NPL == 4) {
+      const float4 u = *reinterpret_cast<const float4 *>(po + static_cast<int64_t>(j) * D);
+      v[0] = u.x;
+      v[1] = u.y;
+      v[NPL - 2] = u.z;
+      v[NPL - 1] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(j) * D);
+      v[0] = u.x;
+      v[1] = u.y;
+    }
     const float f = ex2(m.x - mx);
     l = fmaf(m.y, f, l);
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) x[k] = fmaf(a.po[(row * a.splits + j) * D + lane + 32 * k], f, x[k]);
+    for (int k = 0; k < NPL; ++k) x[k] = fmaf(v[k], f, x[k]);
   }
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) dsc[warp][NPL * lane + k] = x[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < NPL; ++k) x[k] = dsc[warp][lane + 32 * k];
   paged_store_row<D>(x, l, a.books, dsc[warp], a.out, a.out_dtype, row, lane);
 }
 
@@ -979,13 +999,27 @@ Plan plan(const tq_codec *c, int N, int num_seqs, int max_len, int Hq, int Hkv) 
   const size_t head = static_cast<size_t>(num_seqs) * p.max_tiles * tile_bytes(c->d);
   p.heads = static_cast<int>(std::min<size_t>(Hkv, std::max<size_t>(1, TILE_SPACE / head)));
   p.tile_space = head * p.heads;
-  // blocks walk the tiles of a query pair; with too few of them for the SMs
-  // the tiles are split (at least 4 a block) and the parts joined.  A dense
-  // rotation always takes the join, which rotates back row by row.
+  // Blocks walk the tiles of a query pair, one block an SM at a time; the tiles may be
+  // split over more blocks and the parts joined.  The number of parts is the one with the
+  // least rounds x (tiles of a block + 8) + parts / 48: a block's start and end cost about
+  // 8 tiles, a part's way through memory 1/48 (fitted at 64 blocks of 128 tiles: 398, 250,
+  // 276, 324 and 395 us in 1, 2, 4, 8 and 16 parts, 2.4 us a tile; 8 blocks of 157 tiles:
+  // 447, 100, 86, 112 us in 1, 11, 16, 24).  Sequences of several lengths fill up the last
+  // round.  A dense rotation always takes the join, which rotates back row by row.
   const int64_t blocks = std::max<int64_t>(1, static_cast<int64_t>(std::min<int64_t>(
       p.units, (N + 2 * p.tok_tile - 1) / (2 * p.tok_tile) + num_seqs - 1)) * p.heads);
-  int64_t want = blocks >= 148 ? 1 : (148 + blocks - 1) / blocks;
-  want = std::min<int64_t>(want, std::max(1, p.max_tiles / 4));
+  const auto cost = [&](int64_t w) {
+    const double full = static_cast<double>(blocks * w) / 148;
+    const double rounds = num_seqs > 1 ? std::max(1.0, full + 0.3) : std::ceil(full);
+    return rounds * (static_cast<double>((p.max_tiles + w - 1) / w) + 8) + (w > 1 ? blocks * w / 48.0 : 0.0);
+  };
+  int64_t want = 1;
+  double least = 0.95 * cost(1);
+  for (int64_t w = 2; w <= std::min(64, p.max_tiles); ++w)
+    if (cost(w) < least) {
+      least = cost(w);
+      want = w;
+    }
   if (c->rot_dev && want == 1) want = 2;
   p.chunk = static_cast<int>((p.max_tiles + want - 1) / want);
   p.splits = (p.max_tiles + p.chunk - 1) / p.chunk;
