@@ -2,7 +2,7 @@
 // section 2.3, decoder; keys add the QJL term):
 //   keys   nu Pi^T (c_k[idx] + coef rho S^T (2 sigma - 1)),  coef = sqrt(pi/2)/d
 //   values nu Pi^T c_v[idx]
-// Two kernels: a warp a row in fp32 (few rows, fp32 answers, dense rotations), and
+// Two kernels: a block a row in fp32 (few rows, fp32 answers, dense rotations), and
 // tiles of 128 rows whose rotation and sketch are tensor-core products (bf16
 // answers of many rows).
 #include <cstdlib>
@@ -29,99 +29,125 @@ struct PagedDequantArgs {
   TqBooks books;
 };
 
-// ------------------------------------------------------------------ a warp a row
+// ------------------------------------------------------------------ few rows
 
-// Block: the key warp and the value warp of a (token, KV head).
+// Blocks walk the (token, KV head) rows.  S^T (2 sigma - 1) is a sum over the rows of S, a
+// quarter a warp, whose rows of S stay in registers from one (token, head) to the next
+// and are loaded before the batch is read; the first warp then finishes the key, the
+// second the value.
 template <int D>
-__global__ void __launch_bounds__(64) paged_dequant_kernel(const __grid_constant__ PagedDequantArgs a) {
-  constexpr int NPL = D / 32;
+__global__ void __launch_bounds__(128, D == 128 ? 4 : 8) paged_dequant_kernel(const __grid_constant__ PagedDequantArgs a, int64_t rows) {
+  constexpr int NPL = D / 32, SR = D / 4;         // rows of S a warp
   __shared__ float dsc[2][D];
-  __shared__ float acc_s[D];
-  const int lane = threadIdx.x & 31, which = threadIdx.x >> 5;
-  const int64_t it = blockIdx.x;
-  const int tok = static_cast<int>(it / a.Hkv), h = static_cast<int>(it % a.Hkv);
-  void *out = which ? a.v_out : a.k_out;
-  if (out == nullptr) return;
-  sm100::pdl_wait();
-  const int s = paged_find_seq(a.p, tok, 1, 0);
-  const SeqSpan sp = paged_span(a.p, s);
-  const int i = tok - sp.row0, pos = sp.len - sp.n + i;
-  if (i < 0 || i >= sp.n) return;
-  const int page = pos >= 0 ? paged_page(a.p, s, pos) : -1;
-  const int P = 1 << a.p.page_shift;
-  const int64_t row = (static_cast<int64_t>(page) * a.Hkv + h) * P + (pos & (P - 1));
-  const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
-  float y[NPL], nu = 0.f;
+  __shared__ float part[2][4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t sr[SR][NPL / 2];                       // columns NPL lane ..
+  const bool sketch = a.books.qjl && a.k_out != nullptr;
+  if (sketch) {
 #pragma unroll
-  for (int k = 0; k < NPL; ++k) y[k] = 0.f;
-  if (page >= 0 && which == 0) {
-    const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.kcode + row * planes * (D / 8));
-    const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row];
-    nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
-    if (a.books.qjl) {
-      // lane: columns NPL lane .. of S, one row of S a step
+    for (int j = 0; j < SR; ++j) {
+      const uint16_t *p = a.S + (warp * SR + j) * D + NPL * lane;
+      if (NPL == 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        sr[j][0] = u.x;
+        sr[j][NPL / 2 - 1] = u.y;
+      } else {
+        sr[j][0] = *reinterpret_cast<const uint32_t *>(p);
+      }
+    }
+  }
+  sm100::pdl_wait();
+  const int P = 1 << a.p.page_shift, mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
+  int buf = 0;
+  for (int64_t it = blockIdx.x; it < rows; it += gridDim.x) {
+    const int tok = static_cast<int>(it / a.Hkv), h = static_cast<int>(it % a.Hkv);
+    const int s = paged_find_seq(a.p, tok, 1, 0);
+    const SeqSpan sp = paged_span(a.p, s);
+    const int i = tok - sp.row0, pos = sp.len - sp.n + i;
+    if (i < 0 || i >= sp.n) continue;
+    const int page = pos >= 0 ? paged_page(a.p, s, pos) : -1;
+    const int64_t row = (static_cast<int64_t>(page) * a.Hkv + h) * P + (pos & (P - 1));
+    const uint32_t *krow = reinterpret_cast<const uint32_t *>(a.kcode + (page >= 0 ? row : 0) * planes * (D / 8));
+    // the first warp's key codes and the second's value codes, loaded ahead of the sum
+    float y[NPL], nu = 0.f, rho = 0.f;
+    const bool mine = page >= 0 && warp < 2 && (warp ? a.v_out : a.k_out) != nullptr;
+#pragma unroll
+    for (int k = 0; k < NPL; ++k) y[k] = 0.f;
+    if (mine) {
+      uint32_t w[4][NPL];
+      if (warp == 0) {
+        const uint32_t sc = reinterpret_cast<const uint32_t *>(a.kscale)[row];
+        nu = tq_half_to_f32(static_cast<uint16_t>(sc & 0xffffu));
+        rho = tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int k = 0; k < NPL; ++k) w[p][k] = p < mbk ? krow[p * NPL + k] >> lane : 0u;
+      } else {
+        const uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D + lane;
+        nu = tq_half_to_f32(a.vnorm[row]);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int k = 0; k < NPL; ++k) w[p][k] = p < a.books.bits_v ? vg[p * D + 32 * k] >> (pos & 31) : 0u;
+      }
+      const float *c = warp ? a.books.cv : a.books.ck;
+#pragma unroll
+      for (int k = 0; k < NPL; ++k) {
+        int idx = 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) idx |= (w[p][k] & 1u) << p;
+        y[k] = c[idx];
+      }
+    }
+    if (sketch && page >= 0) {
+      const uint32_t sg = krow[mbk * NPL + warp * SR / 32] >> (warp * SR % 32);
       float z[NPL];
 #pragma unroll
       for (int k = 0; k < NPL; ++k) z[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < NPL; ++w) {
-        const uint32_t sg = krow[mbk * NPL + w];
-        const uint16_t *sr = a.S + w * 32 * D + NPL * lane;
-#pragma unroll 16
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t neg = (~(sg >> j) & 1u) << 31;
-          uint32_t v[NPL / 2];
-          if (NPL == 4) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(sr + j * D);
-            v[0] = u.x;
-            v[NPL / 2 - 1] = u.y;
-          } else {
-            v[0] = *reinterpret_cast<const uint32_t *>(sr + j * D);
-          }
+      for (int j = 0; j < SR; ++j) {
+        const uint32_t neg = (~(sg >> j) & 1u) << 31;
 #pragma unroll
-          for (int k = 0; k < NPL / 2; ++k) {
-            z[2 * k] += __uint_as_float((v[k] << 16) ^ neg);
-            z[2 * k + 1] += __uint_as_float((v[k] & 0xffff0000u) ^ neg);
-          }
+        for (int k = 0; k < NPL / 2; ++k) {
+          z[2 * k] += __uint_as_float((sr[j][k] << 16) ^ neg);
+          z[2 * k + 1] += __uint_as_float((sr[j][k] & 0xffff0000u) ^ neg);
         }
       }
 #pragma unroll
-      for (int k = 0; k < NPL; ++k) acc_s[NPL * lane + k] = z[k];
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < NPL; ++k) y[k] = acc_s[lane + 32 * k];
+      for (int k = 0; k < NPL; ++k) part[buf][warp][NPL * lane + k] = z[k];
     }
-    const float f = a.qjl_coef * tq_half_to_f32(static_cast<uint16_t>(sc >> 16));
+    // (two buffers: a warp that writes this one again is past the next row's barrier)
+    __syncthreads();
+    if (warp < 2) {
+      if (warp == 0 && sketch && page >= 0) {
+        const float f = a.qjl_coef * rho;
 #pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      int idx = 0;
-      for (int p = 0; p < mbk; ++p) idx |= ((krow[p * NPL + k] >> lane) & 1) << p;
-      y[k] = fmaf(f, y[k], a.books.ck[idx]);
+        for (int k = 0; k < NPL; ++k) {
+          const int c = lane + 32 * k;
+          y[k] = fmaf(f, (part[buf][0][c] + part[buf][1][c]) + (part[buf][2][c] + part[buf][3][c]), y[k]);
+        }
+      }
+      void *out = warp ? a.v_out : a.k_out;
+      if (out != nullptr) {
+        if (a.books.pi != nullptr) {
+          tq_warp_dense<NPL>(y, a.books.pi, dsc[warp], lane);
+        } else {
+          tq_warp_wht<NPL>(y, lane);
+          tq_apply_signs<NPL>(y, a.books.dneg, lane);
+          nu *= 1.0f / sqrtf(static_cast<float>(D));
+        }
+#pragma unroll
+        for (int k = 0; k < NPL; ++k) {
+          const int64_t o = it * D + lane + 32 * k;
+          if (a.out_dtype == TQ_BF16)
+            static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(y[k] * nu);
+          else
+            static_cast<float *>(out)[o] = y[k] * nu;
+        }
+      }
     }
-  } else if (page >= 0) {
-    const uint32_t *vg = a.vcode + (row >> 5) * a.books.bits_v * D;
-    nu = tq_half_to_f32(a.vnorm[row]);
-#pragma unroll
-    for (int k = 0; k < NPL; ++k) {
-      int idx = 0;
-      for (int p = 0; p < a.books.bits_v; ++p) idx |= ((vg[p * D + lane + 32 * k] >> (pos & 31)) & 1) << p;
-      y[k] = a.books.cv[idx];
-    }
-  }
-  if (a.books.pi != nullptr) {
-    tq_warp_dense<NPL>(y, a.books.pi, dsc[which], lane);
-  } else {
-    tq_warp_wht<NPL>(y, lane);
-    tq_apply_signs<NPL>(y, a.books.dneg, lane);
-    nu *= 1.0f / sqrtf(static_cast<float>(D));
-  }
-#pragma unroll
-  for (int k = 0; k < NPL; ++k) {
-    const int64_t o = it * D + lane + 32 * k;
-    if (a.out_dtype == TQ_BF16)
-      static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(y[k] * nu);
-    else
-      static_cast<float *>(out)[o] = y[k] * nu;
+    buf ^= 1;
   }
 }
 
@@ -448,7 +474,9 @@ int launch_paged_dequant(const tq_codec *c, const PagedView &p, const tq_cache *
     return c->d == 64 ? run_tiles_d<64>(a, k4, v4, stream) : run_tiles_d<128>(a, k4, v4, stream);
   }
   auto kern = c->d == 64 ? paged_dequant_kernel<64> : paged_dequant_kernel<128>;
-  if (tq_launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(64), 0, stream, a) != cudaSuccess)
+  // as many blocks as the SMs hold (by registers), so that S is read once each
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, 148 * (c->d == 64 ? 8 : 4)));
+  if (tq_launch_pdl(kern, dim3(grid), dim3(128), 0, stream, a, rows) != cudaSuccess)
     return tq_check_launch("paged_dequant_kernel");
   tq_count_launch(1);
   return tq_check_launch("paged_dequant_kernel");

@@ -89,6 +89,13 @@ __global__ void __launch_bounds__(128) paged_quantize_kernel(const __grid_consta
     for (int q = 0; q < D / 8; ++q) srow[q] = sp[q];
   }
   sm100::pdl_wait();
+  // the row itself, loaded before its place is known (it lies inside the tensor either way)
+  float xr[1][NPL];
+  const int64_t off = tok * a.st + h * a.sh;
+  {
+    const int64_t offs[1] = {warp < 2 ? off : -1};
+    paged_load_rows<1, NPL>(xr, warp == 0 ? a.k : a.v, offs, a.dtype, lane);
+  }
   const int s = paged_find_seq(a.p, tok, 1, 0);
   const SeqSpan sp = paged_span(a.p, s);
   const int i = tok - sp.row0, pos = sp.len - sp.n + i;
@@ -101,17 +108,14 @@ __global__ void __launch_bounds__(128) paged_quantize_kernel(const __grid_consta
   const int P = 1 << a.p.page_shift;
   const int64_t row = (static_cast<int64_t>(page) * a.Hkv + h) * P + (pos & (P - 1));
   const int mbk = a.books.mse_bits_k, planes = mbk + a.books.qjl;
-  const int64_t off = tok * a.st + h * a.sh;
   const float band = border_band<D>(a.books);
   uint32_t *krow = reinterpret_cast<uint32_t *>(a.kcode + row * planes * (D / 8));
   sm100::pdl_trigger();
   if (warp < 2) {
-    float xr[1][NPL];
     float (&x)[NPL] = xr[0];
     const void *src = warp == 0 ? a.k : a.v;
     const int64_t offs[1] = {off};
     const int poss[1] = {pos};
-    paged_load_rows<1, NPL>(xr, src, offs, a.dtype, lane);
     if (warp == 0) paged_rope_rows<1, NPL>(xr, a.rc, a.rs, poss, offs, lane);
     bool bad, again;
     float nu = unit_f32<NPL>(x, a.books, fscr[warp], lane, bad, again);
