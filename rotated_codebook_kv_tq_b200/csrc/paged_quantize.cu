@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(128) paged_quantize_kernel(const __grid_consta
   __shared__ double buf[2][D];
   __shared__ __align__(16) float rsm[D];
   __shared__ float fscr[2][D], rho_s;
-  __shared__ uint32_t sgw[NPL];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tok = static_cast<int>(blockIdx.x / a.Hkv), h = static_cast<int>(blockIdx.x % a.Hkv);
   // row tid of S, loaded up front: its latency runs under the row's
