@@ -716,25 +716,38 @@ __global__ void __launch_bounds__(384, 1) paged_prefill_kernel(const __grid_cons
       const int j = lane % LPR;
       uint8_t *qimg = sm + L::Q + x * 2 * L::OPER;
       const uint32_t magic = 65535u / a.G + 1u;      // r / G = r magic >> 16 for r, G <= 128
-#pragma unroll 1
-      for (int rb = 32 * lq; rb < 32 * lq + 32; rb += QR) {
+      // (the next rows and their angles are loaded under the rotation of these)
+      float next_v[2][8], next_cs[2][8];     // row; cos, sin
+      const auto load = [&](int rb) {
         const int r = rb + lane / LPR, tt = static_cast<int>((r * magic) >> 16), gh = r - tt * a.G;
         const int tok = tok0 + x * a.tok_tile + tt, at = pos0 + tok;
         const bool on = tt < a.tok_tile && tok < sp.n && at >= 0;
-        float v[2][8];
-        load_halves<D>(v, a.q, on ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + gh) * a.sh + 8 * j : -1,
+        load_halves<D>(next_v, a.q, on ? static_cast<int64_t>(sp.row0 + tok) * a.st + (kvh * a.G + gh) * a.sh + 8 * j : -1,
                        a.dtype, a.q_vec);
         if (a.rc != nullptr) {
-          float cs[2][8];      // cos, sin
           const int64_t ro = static_cast<int64_t>(on ? at : 0) * (D / 2) + 8 * j;
-          load_table(cs, a.rc + ro, a.rs + ro, a.rope_vec);
+          load_table(next_cs, a.rc + ro, a.rs + ro, a.rope_vec);
+        }
+      };
+      load(32 * lq);
+#pragma unroll 1
+      for (int rb = 32 * lq; rb < 32 * lq + 32; rb += QR) {
+        const int r = rb + lane / LPR;
+        float v[2][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[0][e] = next_v[0][e];
+          v[1][e] = next_v[1][e];
+        }
+        if (a.rc != nullptr) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float p = v[0][e], w = v[1][e];
-            v[0][e] = p * cs[0][e] - w * cs[1][e];
-            v[1][e] = w * cs[0][e] + p * cs[1][e];
+            v[0][e] = p * next_cs[0][e] - w * next_cs[1][e];
+            v[1][e] = w * next_cs[0][e] + p * next_cs[1][e];
           }
         }
+        if (rb + QR < 32 * lq + 32) load(rb + QR);
         float f = a.scale * 1.4426950408889634f;
         if (a.books.pi != nullptr) {
           rotate_dense<D>(v, a.books.pi_t, lane);
